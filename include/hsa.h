@@ -333,6 +333,89 @@ enum { HSA_EPI_STORE = 0, HSA_EPI_GELU = 1, HSA_EPI_RESID = 2, HSA_EPI_F32 = 3 }
 int hsa_linear(const void* d_x, int M, int Kin, const void* d_w, int Nout, const float* d_b,
                int dtype, int epilogue, const float* d_gate, void* d_y, void* stream);
 
+/* ------------------------------------------------------------------ block-sparse attention
+ * Attention of compacted queries over chosen blocks of the cache, for grids so long that even |A_i| N
+ * is too much.  Not in the pages: three calls that stand beside hsa_attention and hand to each other,
+ *   hsa_block_scores -> (caller's own masks: -inf closes a block) -> hsa_block_select ->
+ *   hsa_sparse_attention.
+ * The queries are taken in tiles of HSA_QUERY_TILE consecutive compacted rows (the last may be
+ * shorter), T = ceil(M / 128) of them; the cache in blocks of block_k = 64 or 128 consecutive rows (the
+ * last may be shorter), B = ceil(L / block_k).  Every head has its own scores and lists.
+ *
+ * Scores: the mean logit of a query tile against a block,
+ *   d_scores[h][t][b] = (mean of the tile's q rows) . (mean of the block's k rows) / sqrt(128),
+ * float32 sums.  d_q: M x 128H, d_k: L x 128H in dtype; d_scores: [H][T][B] float32.
+ * T + B <= 65535.  Workspace: hsa_block_scores_workspace_size(M, L, H, block_k) bytes (the means). */
+enum { HSA_QUERY_TILE = 128, HSA_SPARSE_MAX_KEEP = 4096 };
+size_t hsa_block_scores_workspace_size(int M, int L, int H, int block_k);
+int hsa_block_scores(const void* d_q, int M, const void* d_k, int L, int H, int dtype, int block_k,
+                     float* d_scores, void* d_ws, size_t ws_bytes, void* stream);
+
+/* The `keep` best blocks of each of `rows` score rows (rows = H T), n_blocks scores each:
+ * ranked by (score descending, block index ascending) -- scores compared as float32, -0 equal to 0,
+ * NaN as +inf -- a score of -inf closes the block.  d_forced[n_blocks] (uint8, device, may be NULL =
+ * none): a block with d_forced[b] != 0 ranks ahead of every other whatever its score, -inf included,
+ * forced blocks among themselves by index (the conditioning frame's blocks, say).
+ *   d_list [rows][keep]  the chosen indices in ascending order, then -1
+ *   d_count[rows]        how many: min(keep, blocks that are open or forced), possibly 0
+ * Bit-exact: the result is unique under this total order.  1 <= n_blocks <= 16384,
+ * 1 <= keep <= HSA_SPARSE_MAX_KEEP (more than n_blocks is allowed). */
+int hsa_block_select(const float* d_scores, int rows, int n_blocks, int keep, const uint8_t* d_forced,
+                     int32_t* d_list, int32_t* d_count, void* stream);
+
+/* o = softmax(q K_S^T / sqrt(128)) V_S per head, S = the rows of the blocks listed for the query's
+ * tile.  d_q: M x 128H, d_k, d_v: L x 128H, d_o: M x 128H in dtype; d_list [H][T][keep], d_count [H][T]
+ * as hsa_block_select writes them.  Any order of a list is accepted; an index listed twice counts its
+ * keys twice; entries behind the count are not read as blocks.  A count of 0 gives rows of 0.  A
+ * listed index outside [0, B) is skipped and a count outside [0, keep] clamped, and both flag HSA_EINDEX.
+ * With a workspace of hsa_sparse_attention_workspace_size(...) bytes the lists of the last, incomplete
+ * wave of work units are split into ranges that a second kernel joins, as in hsa_attention_ws (a few
+ * rows against a long list need it); a smaller or NULL workspace runs every list whole. */
+size_t hsa_sparse_attention_workspace_size(int M, int L, int H, int dtype, int block_k, int keep);
+int hsa_sparse_attention(const void* d_q, int M, const void* d_k, const void* d_v, int L, int H, int dtype,
+                         int block_k, const int32_t* d_list, int keep, const int32_t* d_count, void* d_o,
+                         void* d_ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ residual update fused with its norms
+ * One pass over the rows from a block's output to the next block's input, for blocks with a norm
+ * before (pre) and after (post) and modulation vectors that differ between tokens:
+ *   z = post(y + b)         HSA_NORM_NONE: y + b; RMS or LAYER: normalised over D, * post_g + post_b
+ *   X_out = res_scale X + gate[s] * z
+ *   out = pre(X_out) * (1 + mul[s]) + add[s]  (modulate != 0), or pre(X_out) * mul[s] + add[s]
+ * with s the row's modulation row: d_mod_row[d_idx[r]] of a table with N entries (d_idx NULL:
+ * d_mod_row[r]; d_mod_row NULL: 0).  gate, mul and add point at n_mod rows of D floats, mod_stride floats
+ * apart (three parts of one [n_mod][6][D] table, say).  Norms: eps 1e-6, LAYER subtracts the mean.
+ * NULL gains are 1, NULL offsets 0, a NULL gate 1.  With pre = HSA_NORM_NONE there is no out (d_out, d_mul
+ * and d_add NULL).  A row whose token or modulation index is out of range is left as it was and flags
+ * HSA_EINDEX.  D % 8 == 0, D <= 12288.  d_X_out may be d_X. */
+enum { HSA_NORM_NONE = 0, HSA_NORM_RMS = 1, HSA_NORM_LAYER = 2 };
+typedef struct hsa_residual_norm_args {
+  const float* d_X;             /* M x D float32 residual stream                              */
+  float* d_X_out;               /* M x D float32, may be d_X                                  */
+  const void* d_y;              /* M x D in dtype_y: the block's output                       */
+  void* d_out;                  /* M x D in dtype_out                                         */
+  int dtype_y;
+  int dtype_out;
+  int M;
+  int D;
+  const float* d_b;             /* [D] or NULL: bias of y                                     */
+  int post;                     /* HSA_NORM_* of y + b                                        */
+  int pre;                      /* HSA_NORM_* of X_out                                        */
+  const float* d_post_g;        /* [D] or NULL                                                */
+  const float* d_post_b;        /* [D] or NULL                                                */
+  const float* d_gate;          /* n_mod rows or NULL                                         */
+  const float* d_mul;           /* n_mod rows or NULL                                         */
+  const float* d_add;           /* n_mod rows or NULL                                         */
+  int modulate;
+  float res_scale;
+  const int32_t* d_mod_row;     /* [N] modulation row of each token, or NULL: row 0           */
+  const int32_t* d_idx;         /* [M] token of each row, or NULL: row r is token r           */
+  int N;                        /* entries of d_mod_row                                       */
+  int n_mod;                    /* modulation rows                                            */
+  int64_t mod_stride;           /* floats from one modulation row to the next                 */
+} hsa_residual_norm_args;
+int hsa_residual_norm(const hsa_residual_norm_args* a, void* stream);
+
 /* Patch model around the blocks (latents with C channels per token):
  * hsa_patch_embed:  X (M x D float32) = x[idx[r]] W_in^T + b_in, W_in [D][C] dtype,
  *                   d_x: N x C float32.

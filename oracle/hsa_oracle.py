@@ -250,6 +250,84 @@ def attention(q, K, V):
     return out
 
 
+# ---------------------------------------------------------------- block-sparse attention, residual norm
+# Not in the pages: operators that stand beside the full-context attention and the LayerNorm.
+
+QUERY_TILE = 128
+
+
+def block_scores(q, k, H: int, block: int) -> np.ndarray:
+    """(H, tiles, blocks) mean logit of each 128-row query tile against each block of `block` keys."""
+    M, L = q.shape[0], k.shape[0]
+    T, B = -(-M // QUERY_TILE), -(-L // block)
+    out = np.zeros((H, T, B))
+    for h in range(H):
+        c = slice(HEAD_DIM * h, HEAD_DIM * (h + 1))
+        qm = np.stack([q[t * QUERY_TILE:(t + 1) * QUERY_TILE, c].astype(F64).mean(0) for t in range(T)])
+        km = np.stack([k[b * block:(b + 1) * block, c].astype(F64).mean(0) for b in range(B)])
+        out[h] = qm @ km.T / np.sqrt(HEAD_DIM)
+    return out
+
+
+def block_select(scores, keep: int, forced=None):
+    """(lists, counts): the `keep` best blocks of each score row by (forced, score descending, index
+    ascending), NaN as +inf, -inf never unless forced; ascending lists filled with -1."""
+    s = np.asarray(scores, np.float32)
+    rows = s.reshape(-1, s.shape[-1])
+    lists = np.full((rows.shape[0], keep), -1, np.int32)
+    counts = np.zeros(rows.shape[0], np.int32)
+    for r, row in enumerate(rows):
+        cand = []
+        for b, v in enumerate(row):
+            first = forced is not None and bool(forced[b])
+            v = np.inf if np.isnan(v) else float(v)
+            if first or v > -np.inf:
+                cand.append((not first, 0.0 if first else -v, b))
+        chosen = sorted(b for _, _, b in sorted(cand)[:keep])
+        lists[r, :len(chosen)] = chosen
+        counts[r] = len(chosen)
+    return lists.reshape(*s.shape[:-1], keep), counts.reshape(s.shape[:-1])
+
+
+def sparse_attention(q, K, V, H: int, block: int, lists, counts, absolute: bool = False) -> np.ndarray:
+    """softmax(q K_S^T / sqrt(128)) V_S per head over the listed blocks of each row's query tile, 0 where
+    the list is empty; with `absolute`, |V| in the place of V (what the weights bound errors by)."""
+    M, L = q.shape[0], K.shape[0]
+    out = np.zeros((M, H * HEAD_DIM))
+    for h in range(H):
+        c = slice(HEAD_DIM * h, HEAD_DIM * (h + 1))
+        for t in range(-(-M // QUERY_TILE)):
+            keys = [j for b in lists[h, t, :counts[h, t]] for j in range(b * block, min((b + 1) * block, L))]
+            if not keys:
+                continue
+            r = slice(t * QUERY_TILE, min((t + 1) * QUERY_TILE, M))
+            x = q[r, c].astype(F64) @ K[keys][:, c].astype(F64).T / np.sqrt(HEAD_DIM)
+            e = np.exp(x - x.max(1, keepdims=True))
+            v = V[keys][:, c].astype(F64)
+            out[r, c] = (e @ (np.abs(v) if absolute else v)) / e.sum(1, keepdims=True)
+    return out
+
+
+def _norm_rows(x, kind: str):
+    if kind == "layer":
+        return layer_norm(x)
+    return x / np.sqrt(np.mean(x * x, axis=-1, keepdims=True) + RMS_EPS) if kind == "rms" else x
+
+
+def residual_norm(X, y, b=None, post="none", post_g=None, post_b=None, res_scale=1.0, gate=None, pre="none",
+                  mul=None, add=None, modulate=True):
+    """(X', h): X' = res_scale X + gate * (post(y + b) * post_g + post_b), h = pre(X') (1 + mul) + add, or
+    pre(X') mul + add.  gate, mul, add: one row per row of X, or one for all."""
+    z = y.astype(F64) + (0.0 if b is None else b)
+    z = _norm_rows(z, post) * (1.0 if post_g is None else post_g) + (0.0 if post_b is None else post_b)
+    Xn = res_scale * X.astype(F64) + (1.0 if gate is None else gate) * z
+    if pre == "none":
+        return Xn, None
+    m = 1.0 if mul is None else (1.0 + mul.astype(F64) if modulate else mul)
+    return Xn, _norm_rows(Xn, pre) * m + (0.0 if add is None else add)
+
+
+
 def context_kv(bw, ctx):
     """Cross-attention keys/values of the text context, projected once per run (k RMSNorm'd)."""
     D = bw.w_o.shape[0]

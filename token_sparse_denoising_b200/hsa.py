@@ -17,6 +17,8 @@ LIB_PATH = os.path.join(PKG, "libhsa.so")
 HSA_OK, HSA_EINVAL, HSA_EINDEX, HSA_ECUDA, HSA_ETIMEOUT, HSA_EWORKSPACE = range(6)
 HSA_F32, HSA_BF16 = 0, 1
 EPI_STORE, EPI_GELU, EPI_RESID, EPI_F32 = range(4)
+NORM_NONE, NORM_RMS, NORM_LAYER = range(3)
+QUERY_TILE, SPARSE_MAX_KEEP = 128, 4096
 
 _lib = None
 vp, i32, u64, f32, sz = C.c_void_p, C.c_int, C.c_uint64, C.c_float, C.c_size_t
@@ -42,6 +44,14 @@ class IterationArgsC(C.Structure):
                 ("d_vhat", vp), ("dsigma", f32), ("d_score", vp), ("K", i32), ("h_group_sizes", vp),
                 ("d_group", vp), ("d_order", vp), ("d_ws", vp), ("ws_bytes", sz), ("d_sel_ws", vp),
                 ("sel_ws_bytes", sz)]
+
+
+class ResidualNormArgsC(C.Structure):
+    _fields_ = [("d_X", vp), ("d_X_out", vp), ("d_y", vp), ("d_out", vp), ("dtype_y", i32), ("dtype_out", i32),
+                ("M", i32), ("D", i32), ("d_b", vp), ("post", i32), ("pre", i32), ("d_post_g", vp),
+                ("d_post_b", vp), ("d_gate", vp), ("d_mul", vp), ("d_add", vp), ("modulate", i32),
+                ("res_scale", f32), ("d_mod_row", vp), ("d_idx", vp), ("N", i32), ("n_mod", i32),
+                ("mod_stride", C.c_int64)]
 
 
 class HostSlotC(C.Structure):
@@ -81,6 +91,12 @@ _SIGS = {
     "hsa_qk_norm_rope_ext": (i32, [vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp]),
     "hsa_rms_rows_ext": (i32, [vp, i32, i32, i32, i32, vp, i32, vp, i32, vp, vp]),
     "hsa_gated_residual": (i32, [vp, vp, i32, i32, vp, vp, vp]),
+    "hsa_block_scores_workspace_size": (sz, [i32, i32, i32, i32]),
+    "hsa_block_scores": (i32, [vp, i32, vp, i32, i32, i32, i32, vp, vp, sz, vp]),
+    "hsa_block_select": (i32, [vp, i32, i32, i32, vp, vp, vp, vp]),
+    "hsa_sparse_attention_workspace_size": (sz, [i32, i32, i32, i32, i32, i32]),
+    "hsa_sparse_attention": (i32, [vp, i32, vp, vp, i32, i32, i32, i32, vp, i32, vp, vp, vp, sz, vp]),
+    "hsa_residual_norm": (i32, [C.POINTER(ResidualNormArgsC), vp]),
     "hsa_iteration_host": (i32, [C.POINTER(IterationArgsC), vp, vp, C.POINTER(HostSlotC), vp, vp, vp]),
 }
 
@@ -357,6 +373,138 @@ def gated_residual(X, y, b=None, gate=None, stream=None):
     M, D = X.shape
     _check(lib().hsa_gated_residual(_ptr(X), _ptr(y), M, D, _ptr(b), _ptr(gate), _stream(stream)),
            "hsa_gated_residual")
+
+
+# ---------------------------------------------------------------- block-sparse attention
+
+def _operand(t, name, shape, dtype):
+    """A contiguous tensor of this shape and type on the current device, whose stream the call uses."""
+    import torch
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _need(t, name, dtype)
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
+
+
+def _block_count(n: int, size: int) -> int:
+    return -(-n // size)
+
+
+def block_scores_workspace_size(M: int, L: int, H: int, block: int) -> int:
+    return int(lib().hsa_block_scores_workspace_size(M, L, H, block))
+
+
+def block_scores(q, k, H: int, block: int, scores, ws=None, stream=None):
+    """scores[h, t, b] = mean logit of query tile t (128 rows of q) against block b (`block` rows of k),
+    float32 (hsa_block_scores); `ws`: uint8, at least block_scores_workspace_size bytes."""
+    import torch
+    M, L = q.shape[0], k.shape[0]
+    code = _dtype_code(q)
+    _operand(q, "q", (M, H * 128), q.dtype)
+    _operand(k, "k", (L, H * 128), q.dtype)
+    _operand(scores, "scores", (H, _block_count(M, QUERY_TILE), _block_count(L, block)), torch.float32)
+    if ws is None:
+        ws = torch.empty(block_scores_workspace_size(M, L, H, block), dtype=torch.uint8, device=q.device)
+    _check(lib().hsa_block_scores(_ptr(q), M, _ptr(k), L, H, code, block, _ptr(scores), _ptr(ws),
+                                  ws.numel() * ws.element_size(), _stream(stream)), "hsa_block_scores")
+
+
+def block_select(scores, keep: int, lists, counts, forced=None, stream=None):
+    """The `keep` best blocks of every score row (hsa_block_select): scores (..., blocks) float32 ->
+    lists (..., keep) and counts (...) int32; `forced` (uint8 [blocks], optional) rank ahead."""
+    import torch
+    lead, B = scores.shape[:-1], scores.shape[-1]
+    _operand(scores, "scores", scores.shape, torch.float32)
+    _operand(lists, "lists", (*lead, keep), torch.int32)
+    _operand(counts, "counts", lead, torch.int32)
+    if forced is not None:
+        _operand(forced, "forced", (B,), torch.uint8)
+    rows = 1
+    for n in lead:
+        rows *= n
+    _check(lib().hsa_block_select(_ptr(scores), rows, B, keep, _ptr(forced), _ptr(lists), _ptr(counts),
+                                  _stream(stream)), "hsa_block_select")
+
+
+def sparse_attention_workspace_size(M: int, L: int, H: int, dtype: int, block: int, keep: int) -> int:
+    return int(lib().hsa_sparse_attention_workspace_size(M, L, H, dtype, block, keep))
+
+
+def sparse_attention(q, k, v, H: int, block: int, lists, counts, o, stream=None, ws=None):
+    """o = softmax(q k_S^T / sqrt(128)) v_S per head over the rows S of the blocks listed for the query's
+    tile (hsa_sparse_attention): lists (H, tiles, keep), counts (H, tiles) int32 as block_select writes
+    them; with `ws` (uint8, at least sparse_attention_workspace_size bytes) long lists of few rows are
+    split."""
+    import torch
+    M, L = q.shape[0], k.shape[0]
+    code = _dtype_code(q)
+    T, keep = _block_count(M, QUERY_TILE), lists.shape[-1]
+    _operand(q, "q", (M, H * 128), q.dtype)
+    _operand(k, "k", (L, H * 128), q.dtype)
+    _operand(v, "v", (L, H * 128), q.dtype)
+    _operand(o, "o", (M, H * 128), q.dtype)
+    _operand(lists, "lists", (H, T, keep), torch.int32)
+    _operand(counts, "counts", (H, T), torch.int32)
+    _check(lib().hsa_sparse_attention(_ptr(q), M, _ptr(k), _ptr(v), L, H, code, block, _ptr(lists), keep,
+                                      _ptr(counts), _ptr(o), _ptr(ws),
+                                      0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
+           "hsa_sparse_attention")
+
+
+# ---------------------------------------------------------------- residual update fused with its norms
+
+_NORMS = {"none": NORM_NONE, "rms": NORM_RMS, "layer": NORM_LAYER}
+
+
+def residual_norm(X, y, X_out=None, out=None, b=None, post="none", post_g=None, post_b=None, res_scale: float = 1.0,
+                  gate=None, pre="none", mul=None, add=None, modulate: bool = True, mod_row=None, idx=None,
+                  stream=None):
+    """X_out = res_scale X + gate * post(y + b); out = pre(X_out) (1 + mul) + add, or pre(X_out) mul + add
+    when not `modulate` (hsa_residual_norm).  post, pre: "none", "rms" or "layer"; X_out defaults to X.
+    gate, mul, add: [D], or (n_mod, D) views of one modulation table (equal row strides) whose row is
+    mod_row[token], token = idx[r] (idx None: r)."""
+    import torch
+    M, D = X.shape
+    X_out = X if X_out is None else X_out
+    if post not in _NORMS or pre not in _NORMS:
+        raise ValueError("post and pre must be 'none', 'rms' or 'layer'")
+    _operand(X, "X", (M, D), torch.float32)
+    _operand(X_out, "X_out", (M, D), torch.float32)
+    _operand(y, "y", (M, D), y.dtype)
+    if out is not None:
+        _operand(out, "out", (M, D), out.dtype)
+    for name, t in (("b", b), ("post_g", post_g), ("post_b", post_b)):
+        if t is not None:
+            _operand(t, name, (D,), torch.float32)
+    stride, n_mod = None, None
+    for name, t in (("gate", gate), ("mul", mul), ("add", add)):
+        if t is None:
+            continue
+        if t.dtype != torch.float32 or t.device != X.device or t.dim() not in (1, 2) or t.shape[-1] != D or \
+                t.stride(-1) != 1:
+            raise ValueError(f"{name} must be float32 rows of {D} on X's device")
+        rows, step = (1, D) if t.dim() == 1 else (t.shape[0], t.stride(0) if t.shape[0] > 1 else D)
+        if n_mod is not None and (rows, step) != (n_mod, stride):
+            raise ValueError("gate, mul and add must have the same rows and row stride")
+        n_mod, stride = rows, step
+    if mod_row is None and n_mod not in (None, 1):
+        raise ValueError("several modulation rows need mod_row")
+    if mod_row is not None and n_mod is None:
+        raise ValueError("mod_row without gate, mul or add")
+    N = 0
+    if mod_row is not None:
+        if mod_row.dim() != 1:
+            raise ValueError("mod_row must be one row number per token")
+        N = mod_row.shape[0]
+        _operand(mod_row, "mod_row", (N,), torch.int32)
+    if idx is not None:
+        _operand(idx, "idx", (M,), torch.int32)
+    a = ResidualNormArgsC(_ptr(X), _ptr(X_out), _ptr(y), _ptr(out), _dtype_code(y),
+                          HSA_F32 if out is None else _dtype_code(out), M, D, _ptr(b), _NORMS[post], _NORMS[pre],
+                          _ptr(post_g), _ptr(post_b), _ptr(gate), _ptr(mul), _ptr(add), 1 if modulate else 0,
+                          res_scale, _ptr(mod_row), _ptr(idx), N, n_mod or 1, stride or D)
+    _check(lib().hsa_residual_norm(C.byref(a), _stream(stream)), "hsa_residual_norm")
 
 
 class HostSlot:
