@@ -8,11 +8,14 @@
 // bytes an element, each once.  hsa_gated_residual followed by hsa_layernorm_rows moves X' twice more
 // (written, read again) and has no post-norm.
 //
-// A row lives in the registers of W warps, 8 columns (16 or 32 bytes) per thread and chunk, so both
+// A row lives in the registers of W warps, 4 columns (one 16-byte access) per thread and chunk, so both
 // norms see all of it without a second read.  W = 1 up to 1536 columns (48 values a thread); wider rows
-// take one block of 2, 4 or 8 warps, and each reduction crosses the warps through shared memory.  All
-// sums are float32, variances of centred values.  The modulation vectors of neighbouring rows are
-// mostly the same, so they come from L1.
+// take 2, 4 or 8 warps, and each reduction crosses them through shared memory.  All sums are float32,
+// variances of centred values.
+// One block of 16 warps per SM walks the rows.  Each group of W warps has its own ring of row slots in
+// shared memory, filled by bulk copies (one elected lane, an mbarrier per slot), so the next row's X
+// and y travel while this row is reduced and written; the copies bypass L1, which keeps the
+// modulation vectors that neighbouring rows share.
 #include "common.cuh"
 
 namespace hsa {
@@ -52,30 +55,33 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
     v[2 * i + 1] = f.y;
   }
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  st4(p, make_float4(v[0], v[1], v[2], v[3]));
-  st4(p + 4, make_float4(v[4], v[5], v[6], v[7]));
-}
-// one rounding to bf16, of the finished value
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  uint4 u;
-  u.x = pack_bf16x2(v[0], v[1]);
-  u.y = pack_bf16x2(v[2], v[3]);
-  u.z = pack_bf16x2(v[4], v[5]);
-  u.w = pack_bf16x2(v[6], v[7]);
-  *reinterpret_cast<uint4*>(p) = u;
+// Bulk copy global -> shared, `bytes` (a multiple of 16) completing on `bar`
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
-// Sum over the W warps of a row.  W > 1: one row per block; the two halves of `part` alternate, so
-// one barrier a reduction is enough.
+constexpr int kRnWarps = 16;        // per block, one block per SM
+constexpr int kRnSlots = 4;         // most row slots a group may have
+constexpr int kRnSmem = 200 * 1024; // of row slots
+
+// The W warps of group g
 template <int W>
-__device__ __forceinline__ float row_sum(float v, float* part, int& turn) {
+__device__ __forceinline__ void group_sync(int g) {
+  if constexpr (W == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "r"(32 * W) : "memory");
+}
+
+// Sum over the W warps of a row; the two halves of `part` alternate, so one barrier a sum is enough
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float* part, int& turn, int g) {
   v = warp_sum(v);
   if constexpr (W > 1) {
     float* p = part + (turn & 1) * W;
     ++turn;
-    if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = v;
-    __syncthreads();
+    if ((threadIdx.x & 31) == 0) p[(threadIdx.x >> 5) % W] = v;
+    group_sync<W>(g);
     v = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) v += p[w];
@@ -83,157 +89,193 @@ __device__ __forceinline__ float row_sum(float v, float* part, int& turn) {
   return v;
 }
 
-// v <- normalised row (no gain): LayerNorm when `layer`, else RMSNorm
+// v <- normalised row (no gain): LayerNorm when `layer`, else RMSNorm.  Columns beyond D hold 0.
 template <int W, int C>
-__device__ __forceinline__ void normalise(float (&v)[C][8], int D, int l, bool layer, float* part, int& turn) {
+__device__ __forceinline__ void normalise(float4 (&v)[C], int D, int l, bool layer, float* part, int& turn, int g) {
   const float inv_d = 1.0f / (float)D;
   if (layer) {
     float s = 0.f;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s += v[c][e];          // columns beyond D hold 0
-    const float mean = row_sum<W>(s, part, turn) * inv_d;
+    for (int c = 0; c < C; ++c) s += (v[c].x + v[c].y) + (v[c].z + v[c].w);
+    const float mean = row_sum<W>(s, part, turn, g) * inv_d;
 #pragma unroll
     for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[c][e] = (8 * (l + c * 32 * W) < D) ? v[c][e] - mean : 0.f;
+      if (4 * (l + c * 32 * W) < D) {
+        v[c].x -= mean; v[c].y -= mean; v[c].z -= mean; v[c].w -= mean;
+      }
   }
   float q = 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c)
+    q = fmaf(v[c].x, v[c].x, fmaf(v[c].y, v[c].y, fmaf(v[c].z, v[c].z, fmaf(v[c].w, v[c].w, q))));
+  const float r = rsqrtf(fmaf(row_sum<W>(q, part, turn, g), inv_d, kNormEps));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q = fmaf(v[c][e], v[c][e], q);
-  const float r = rsqrtf(fmaf(row_sum<W>(q, part, turn), inv_d, kNormEps));
+  for (int c = 0; c < C; ++c) {
+    v[c].x *= r; v[c].y *= r; v[c].z *= r; v[c].w *= r;
+  }
+}
+
+__device__ __forceinline__ float4 fma4(float4 a, float4 b, float4 c) {
+  return make_float4(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y), fmaf(a.z, b.z, c.z), fmaf(a.w, b.w, c.w));
+}
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+__device__ __forceinline__ float4 mul4(float4 a, float4 b) {
+  return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
+}
+
+// f(z[c], v[col]) for the thread's chunks of a row vector, `kRnBatch` loads in flight at a time (a load
+// that waits for the use before it costs an L1 round trip per chunk: 221 against 111 us at 32760 x 1536)
+constexpr int kRnBatch = 4;
+template <int W, int C, typename F>
+__device__ __forceinline__ void with_vector(float4 (&z)[C], const float* v, int D, int l, F&& f) {
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c0 = 0; c0 < C; c0 += kRnBatch) {
+    float4 t[kRnBatch];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[c][e] *= r;
+    for (int i = 0; i < kRnBatch; ++i) {
+      const int col = 4 * (l + (c0 + i) * 32 * W);
+      t[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c0 + i < C && col < D) t[i] = ld4(v + col);
+    }
+#pragma unroll
+    for (int i = 0; i < kRnBatch; ++i)
+      if (c0 + i < C) z[c0 + i < C ? c0 + i : 0] = f(z[c0 + i < C ? c0 + i : 0], t[i]);
+  }
 }
 
 template <int W, int C, typename TY, typename TO>
-__global__ void __launch_bounds__(W == 1 ? 256 : 32 * W)
-    k_residual_norm(const ResNormArgs a, const TY* y, TO* out) {
+__global__ void __launch_bounds__(32 * kRnWarps, 1) k_residual_norm(const ResNormArgs a, const TY* y, TO* out, int slots) {
   pdl_prologue();
-  __shared__ float part[W > 1 ? 2 * W : 1];
-  int turn = 0;
-  const int r = W == 1 ? (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5) : (int)blockIdx.x;
-  const int l = W == 1 ? (threadIdx.x & 31) : threadIdx.x;
-  if (r >= a.M) return;
-  const int D = a.D;
-  // modulation row of this token
-  int64_t m_off = 0;
-  if (a.mod_row) {
-    const int n = a.idx ? a.idx[r] : r;
-    const int m = (n >= 0 && n < a.N) ? a.mod_row[n] : -1;
-    if (m < 0 || m >= a.n_mod) {
-      if (l == 0) flag_error(HSA_EINDEX);
-      return;                                            // the same for every thread of the row
-    }
-    m_off = m * a.mod_stride;
+  constexpr int G = kRnWarps / W;
+  extern __shared__ __align__(128) uint8_t rn_smem[];
+  __shared__ uint64_t full[G][kRnSlots];
+  __shared__ float parts[G][2 * W];
+  const int D = a.D, M = a.M;
+  const int g = threadIdx.x / (32 * W), l = threadIdx.x % (32 * W);
+  const size_t slot_bytes = (size_t)D * (4 + sizeof(TY));
+  uint8_t* ring = rn_smem + (size_t)g * slots * slot_bytes;
+  float* part = parts[g];
+  if (l == 0) {
+    for (int s = 0; s < slots; ++s) mbar_init(&full[g][s], 1);
+    fence_mbar_init();
   }
-  const size_t base = (size_t)r * D;
-  float z[C][8];
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int col = 8 * (l + c * 32 * W);
-    if (col < D) {
-      load8(y + base + col, z[c]);
-      if (a.b) {
-        float t[8];
-        load8(a.b + col, t);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[c][e] += t[e];
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[c][e] = 0.f;
+  group_sync<W>(g);
+  // the group's rows: first, first + step, ...: consecutive rows go to different SMs
+  const int first = g * (int)gridDim.x + (int)blockIdx.x, step = G * (int)gridDim.x;
+  auto load_row = [&](int64_t r, int s) {
+    uint8_t* p = ring + s * slot_bytes;
+    mbar_expect_tx(&full[g][s], (uint32_t)slot_bytes);
+    bulk_load(p, a.X + (size_t)r * D, (uint32_t)D * 4, &full[g][s]);
+    bulk_load(p + (size_t)D * 4, y + (size_t)r * D, (uint32_t)D * sizeof(TY), &full[g][s]);
+  };
+  if (l == 0)
+    for (int s = 0; s < slots; ++s) {
+      const int64_t r = first + (int64_t)s * step;
+      if (r < M) load_row(r, s);
     }
-  }
-  if (a.post != HSA_NORM_NONE) {
-    normalise<W, C>(z, D, l, a.post == HSA_NORM_LAYER, part, turn);
+  int turn = 0, s = 0;
+  uint32_t phase = 0;
+  const float one = a.modulate ? 1.0f : 0.0f;
+  for (int64_t r = first; r < M; r += step) {
+    // modulation row of this token; `good` is the same for the whole group
+    int64_t m_off = 0;
+    bool good = true;
+    if (a.mod_row) {
+      const int n = a.idx ? a.idx[r] : (int)r;
+      const int m = (n >= 0 && n < a.N) ? a.mod_row[n] : -1;
+      good = m >= 0 && m < a.n_mod;
+      if (good) m_off = m * a.mod_stride;
+      else if (l == 0) flag_error(HSA_EINDEX);
+    }
+    const float* xs = reinterpret_cast<const float*>(ring + s * slot_bytes);
+    const TY* ys = reinterpret_cast<const TY*>(xs + D);
+    mbar_wait(&full[g][s], phase);                        // gives up only once the library has stalled
+    __syncwarp();
+    const size_t base = (size_t)r * D;
+    float4 z[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int col = 8 * (l + c * 32 * W);
-      if (col < D) {
-        float t[8];
-        if (a.post_g) {
-          load8(a.post_g + col, t);
+      const int col = 4 * (l + c * 32 * W);
+      z[c] = col < D ? load4(ys + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (a.b) with_vector<W, C>(z, a.b, D, l, add4);
+    if (a.post != HSA_NORM_NONE) {
+      normalise<W, C>(z, D, l, a.post == HSA_NORM_LAYER, part, turn, g);
+      if (a.post_g) with_vector<W, C>(z, a.post_g, D, l, mul4);
+      if (a.post_b) with_vector<W, C>(z, a.post_b, D, l, add4);
+    }
+    if (a.gate) with_vector<W, C>(z, a.gate + m_off, D, l, mul4);
+    const float4 scale = make_float4(a.res_scale, a.res_scale, a.res_scale, a.res_scale);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z[c][e] *= t[e];
-        }
-        if (a.post_b) {
-          load8(a.post_b + col, t);
+    for (int c = 0; c < C; ++c) {
+      const int col = 4 * (l + c * 32 * W);
+      if (col < D) z[c] = fma4(scale, ld4(xs + col), z[c]);
+    }
+    // the row is in registers: its slot takes the row `slots` further on
+    group_sync<W>(g);
+    if (l == 0 && r + (int64_t)slots * step < M) load_row(r + (int64_t)slots * step, s);
+    if (++s == slots) {
+      s = 0;
+      phase ^= 1;
+    }
+    if (good) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z[c][e] += t[e];
-        }
+      for (int c = 0; c < C; ++c) {
+        const int col = 4 * (l + c * 32 * W);
+        if (col < D) st4(a.X_out + base + col, z[c]);
       }
     }
-  }
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int col = 8 * (l + c * 32 * W);
-    if (col < D) {
-      float x[8], t[8];
-      load8(a.X + base + col, x);
-      if (a.gate) {
-        load8(a.gate + m_off + col, t);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[c][e] *= t[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[c][e] = fmaf(a.res_scale, x[e], z[c][e]);
-      store8(a.X_out + base + col, z[c]);
+    if (a.pre == HSA_NORM_NONE) continue;
+    normalise<W, C>(z, D, l, a.pre == HSA_NORM_LAYER, part, turn, g);
+    if (!good) continue;
+    if (a.mul) {
+      with_vector<W, C>(z, a.mul + m_off, D, l, [one](float4 v, float4 t) {
+        return mul4(v, make_float4(one + t.x, one + t.y, one + t.z, one + t.w));
+      });
     }
-  }
-  if (a.pre == HSA_NORM_NONE) return;
-  normalise<W, C>(z, D, l, a.pre == HSA_NORM_LAYER, part, turn);
-  const float one = a.modulate ? 1.0f : 0.0f;
+    if (a.add) with_vector<W, C>(z, a.add + m_off, D, l, add4);
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int col = 8 * (l + c * 32 * W);
-    if (col < D) {
-      float t[8];
-      if (a.mul) {
-        load8(a.mul + m_off + col, t);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[c][e] *= one + t[e];
-      }
-      if (a.add) {
-        load8(a.add + m_off + col, t);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[c][e] += t[e];
-      }
-      store8(out + base + col, z[c]);
+    for (int c = 0; c < C; ++c) {
+      const int col = 4 * (l + c * 32 * W);
+      if (col < D) store4(out + base + col, z[c]);        // one rounding, of the finished value
     }
   }
 }
 
 template <int W, int C, typename TY, typename TO>
-static void launch_resnorm(const ResNormArgs& a, const void* y, void* out, cudaStream_t st) {
-  const unsigned rows_per_block = W == 1 ? 8 : 1;
-  launch(k_residual_norm<W, C, TY, TO>, ((unsigned)a.M + rows_per_block - 1) / rows_per_block, W == 1 ? 256 : 32 * W, 0,
-         st, a, static_cast<const TY*>(y), static_cast<TO*>(out));
+static int launch_resnorm(const ResNormArgs& a, const void* y, void* out, cudaStream_t st) {
+  static PerContextOnce attr;
+  int rc = attr.ensure([](void**) {
+    if (cudaFuncSetAttribute(k_residual_norm<W, C, TY, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRnSmem) !=
+        cudaSuccess)
+      return check_launch("residual_norm: shared-memory attribute");
+    return (int)HSA_OK;
+  });
+  if (rc) return rc;
+  constexpr int G = kRnWarps / W;
+  const size_t slot = (size_t)a.D * (4 + sizeof(TY)) * G;
+  int slots = (int)(kRnSmem / slot);
+  slots = slots < 1 ? 1 : slots > kRnSlots ? kRnSlots : slots;
+  const int blocks = a.M < num_sms() ? a.M : num_sms();
+  launch(k_residual_norm<W, C, TY, TO>, (unsigned)blocks, 32 * kRnWarps, slots * slot, st, a,
+         static_cast<const TY*>(y), static_cast<TO*>(out), slots);
+  return HSA_OK;
 }
 
-// W: the fewest warps whose threads hold at most 48 values; C: chunks of 8 columns a thread
+// W: the fewest warps whose threads hold at most 48 values; C: chunks of 4 columns a thread
 template <typename TY, typename TO>
-static void dispatch_resnorm(const ResNormArgs& a, const void* y, void* out, cudaStream_t st) {
+static int dispatch_resnorm(const ResNormArgs& a, const void* y, void* out, cudaStream_t st) {
   const int D = a.D;
-  const int W = D <= kResNormWarpD ? 1 : D <= 2 * kResNormWarpD ? 2 : D <= 4 * kResNormWarpD ? 4 : 8;
-  const int C = (D + 256 * W - 1) / (256 * W);
-  if (W == 1) {
-    if (C <= 2) launch_resnorm<1, 2, TY, TO>(a, y, out, st);
-    else if (C <= 4) launch_resnorm<1, 4, TY, TO>(a, y, out, st);
-    else launch_resnorm<1, 6, TY, TO>(a, y, out, st);
-  } else if (W == 2) {
-    launch_resnorm<2, 6, TY, TO>(a, y, out, st);
-  } else if (W == 4) {
-    if (C <= 5) launch_resnorm<4, 5, TY, TO>(a, y, out, st);
-    else launch_resnorm<4, 6, TY, TO>(a, y, out, st);
-  } else {
-    launch_resnorm<8, 6, TY, TO>(a, y, out, st);
-  }
+  if (D <= 256) return launch_resnorm<1, 2, TY, TO>(a, y, out, st);
+  if (D <= 512) return launch_resnorm<1, 4, TY, TO>(a, y, out, st);
+  if (D <= 1024) return launch_resnorm<1, 8, TY, TO>(a, y, out, st);
+  if (D <= kResNormWarpD) return launch_resnorm<1, 12, TY, TO>(a, y, out, st);
+  if (D <= 2 * kResNormWarpD) return launch_resnorm<2, 12, TY, TO>(a, y, out, st);
+  if (D <= 5120) return launch_resnorm<4, 10, TY, TO>(a, y, out, st);
+  if (D <= 4 * kResNormWarpD) return launch_resnorm<4, 12, TY, TO>(a, y, out, st);
+  return launch_resnorm<8, 12, TY, TO>(a, y, out, st);
 }
 
 }  // namespace hsa
@@ -269,10 +311,11 @@ extern "C" int hsa_residual_norm(const hsa_residual_norm_args* p, void* stream) 
                 p->d_idx, p->res_scale, p->M, p->D, p->N, p->n_mod, p->post, p->pre, p->modulate, p->mod_stride};
   ScopedTiming timing(HSA_KCLASS_OTHER, st);
   using bf16 = __nv_bfloat16;
-  if (y_bf && o_bf) dispatch_resnorm<bf16, bf16>(a, p->d_y, p->d_out, st);
-  else if (y_bf) dispatch_resnorm<bf16, float>(a, p->d_y, p->d_out, st);
-  else if (o_bf) dispatch_resnorm<float, bf16>(a, p->d_y, p->d_out, st);
-  else dispatch_resnorm<float, float>(a, p->d_y, p->d_out, st);
+  const int rc = y_bf ? (o_bf ? dispatch_resnorm<bf16, bf16>(a, p->d_y, p->d_out, st)
+                              : dispatch_resnorm<bf16, float>(a, p->d_y, p->d_out, st))
+                      : (o_bf ? dispatch_resnorm<float, bf16>(a, p->d_y, p->d_out, st)
+                              : dispatch_resnorm<float, float>(a, p->d_y, p->d_out, st));
+  if (rc) return rc;
   count_launch(1);
   return check_launch("residual_norm launch");
 }
