@@ -377,14 +377,26 @@ def gated_residual(X, y, b=None, gate=None, stream=None):
 
 # ---------------------------------------------------------------- block-sparse attention
 
-def _operand(t, name, shape, dtype):
-    """A contiguous tensor of this shape and type on the current device, whose stream the call uses."""
-    import torch
-    if tuple(t.shape) != tuple(shape):
+# A call of these operators takes the GPU a few microseconds, so the checks of their arguments are kept
+# to a few comparisons each; _refuse says what is wrong once one has failed.
+
+def _bad(t, shape, dtype, dev: int) -> bool:
+    return not (t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev)
+
+
+def _refuse(t, name, shape, dtype, dev: int):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     _need(t, name, dtype)
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device, got {t.device}")
+    raise ValueError(f"{name} must be on the device of the first operand, got {t.device}")
+
+
+def _current(dev: int, stream) -> int:
+    """The stream handle of a call on tensors of device `dev`, which has to be the current one."""
+    import torch
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"the operands must be on the current CUDA device, got device {dev}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _block_count(n: int, size: int) -> int:
@@ -399,32 +411,34 @@ def block_scores(q, k, H: int, block: int, scores, ws=None, stream=None):
     """scores[h, t, b] = mean logit of query tile t (128 rows of q) against block b (`block` rows of k),
     float32 (hsa_block_scores); `ws`: uint8, at least block_scores_workspace_size bytes."""
     import torch
-    M, L = q.shape[0], k.shape[0]
+    M, L, D, dt, dev = q.shape[0], k.shape[0], H * 128, q.dtype, q.get_device()
     code = _dtype_code(q)
-    _operand(q, "q", (M, H * 128), q.dtype)
-    _operand(k, "k", (L, H * 128), q.dtype)
-    _operand(scores, "scores", (H, _block_count(M, QUERY_TILE), _block_count(L, block)), torch.float32)
+    if block not in (64, 128):
+        raise ValueError("block must be 64 or 128")
+    out = (H, _block_count(M, QUERY_TILE), _block_count(L, block))
+    if _bad(q, (M, D), dt, dev): _refuse(q, "q", (M, D), dt, dev)
+    if _bad(k, (L, D), dt, dev): _refuse(k, "k", (L, D), dt, dev)
+    if _bad(scores, out, torch.float32, dev): _refuse(scores, "scores", out, torch.float32, dev)
+    st = _current(dev, stream)
     if ws is None:
         ws = torch.empty(block_scores_workspace_size(M, L, H, block), dtype=torch.uint8, device=q.device)
-    _check(lib().hsa_block_scores(_ptr(q), M, _ptr(k), L, H, code, block, _ptr(scores), _ptr(ws),
-                                  ws.numel() * ws.element_size(), _stream(stream)), "hsa_block_scores")
+    _check(lib().hsa_block_scores(q.data_ptr(), M, k.data_ptr(), L, H, code, block, scores.data_ptr(), ws.data_ptr(),
+                                  ws.numel() * ws.element_size(), st), "hsa_block_scores")
 
 
 def block_select(scores, keep: int, lists, counts, forced=None, stream=None):
     """The `keep` best blocks of every score row (hsa_block_select): scores (..., blocks) float32 ->
     lists (..., keep) and counts (...) int32; `forced` (uint8 [blocks], optional) rank ahead."""
     import torch
-    lead, B = scores.shape[:-1], scores.shape[-1]
-    _operand(scores, "scores", scores.shape, torch.float32)
-    _operand(lists, "lists", (*lead, keep), torch.int32)
-    _operand(counts, "counts", lead, torch.int32)
-    if forced is not None:
-        _operand(forced, "forced", (B,), torch.uint8)
-    rows = 1
-    for n in lead:
-        rows *= n
-    _check(lib().hsa_block_select(_ptr(scores), rows, B, keep, _ptr(forced), _ptr(lists), _ptr(counts),
-                                  _stream(stream)), "hsa_block_select")
+    shape, dev = scores.shape, scores.get_device()
+    lead, B, i32t = shape[:-1], shape[-1], torch.int32
+    if _bad(scores, shape, torch.float32, dev): _refuse(scores, "scores", shape, torch.float32, dev)
+    if _bad(lists, (*lead, keep), i32t, dev): _refuse(lists, "lists", (*lead, keep), i32t, dev)
+    if _bad(counts, lead, i32t, dev): _refuse(counts, "counts", lead, i32t, dev)
+    if forced is not None and _bad(forced, (B,), torch.uint8, dev): _refuse(forced, "forced", (B,), torch.uint8, dev)
+    st = _current(dev, stream)
+    _check(lib().hsa_block_select(scores.data_ptr(), counts.numel(), B, keep, _ptr(forced), lists.data_ptr(),
+                                  counts.data_ptr(), st), "hsa_block_select")
 
 
 def sparse_attention_workspace_size(M: int, L: int, H: int, dtype: int, block: int, keep: int) -> int:
@@ -437,18 +451,19 @@ def sparse_attention(q, k, v, H: int, block: int, lists, counts, o, stream=None,
     them; with `ws` (uint8, at least sparse_attention_workspace_size bytes) long lists of few rows are
     split."""
     import torch
-    M, L = q.shape[0], k.shape[0]
-    code = _dtype_code(q)
-    T, keep = _block_count(M, QUERY_TILE), lists.shape[-1]
-    _operand(q, "q", (M, H * 128), q.dtype)
-    _operand(k, "k", (L, H * 128), q.dtype)
-    _operand(v, "v", (L, H * 128), q.dtype)
-    _operand(o, "o", (M, H * 128), q.dtype)
-    _operand(lists, "lists", (H, T, keep), torch.int32)
-    _operand(counts, "counts", (H, T), torch.int32)
-    _check(lib().hsa_sparse_attention(_ptr(q), M, _ptr(k), _ptr(v), L, H, code, block, _ptr(lists), keep,
-                                      _ptr(counts), _ptr(o), _ptr(ws),
-                                      0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
+    M, L, D, dt, dev = q.shape[0], k.shape[0], H * 128, q.dtype, q.get_device()
+    code, keep, i32t = _dtype_code(q), lists.shape[-1], torch.int32
+    T = _block_count(M, QUERY_TILE)
+    if _bad(q, (M, D), dt, dev): _refuse(q, "q", (M, D), dt, dev)
+    if _bad(k, (L, D), dt, dev): _refuse(k, "k", (L, D), dt, dev)
+    if _bad(v, (L, D), dt, dev): _refuse(v, "v", (L, D), dt, dev)
+    if _bad(o, (M, D), dt, dev): _refuse(o, "o", (M, D), dt, dev)
+    if _bad(lists, (H, T, keep), i32t, dev): _refuse(lists, "lists", (H, T, keep), i32t, dev)
+    if _bad(counts, (H, T), i32t, dev): _refuse(counts, "counts", (H, T), i32t, dev)
+    st = _current(dev, stream)
+    _check(lib().hsa_sparse_attention(q.data_ptr(), M, k.data_ptr(), v.data_ptr(), L, H, code, block,
+                                      lists.data_ptr(), keep, counts.data_ptr(), o.data_ptr(), _ptr(ws),
+                                      0 if ws is None else ws.numel() * ws.element_size(), st),
            "hsa_sparse_attention")
 
 
@@ -466,45 +481,44 @@ def residual_norm(X, y, X_out=None, out=None, b=None, post="none", post_g=None, 
     mod_row[token], token = idx[r] (idx None: r)."""
     import torch
     M, D = X.shape
-    X_out = X if X_out is None else X_out
+    f32t, dev = torch.float32, X.get_device()
     if post not in _NORMS or pre not in _NORMS:
         raise ValueError("post and pre must be 'none', 'rms' or 'layer'")
-    _operand(X, "X", (M, D), torch.float32)
-    _operand(X_out, "X_out", (M, D), torch.float32)
-    _operand(y, "y", (M, D), y.dtype)
-    if out is not None:
-        _operand(out, "out", (M, D), out.dtype)
-    for name, t in (("b", b), ("post_g", post_g), ("post_b", post_b)):
-        if t is not None:
-            _operand(t, name, (D,), torch.float32)
-    stride, n_mod = None, None
-    for name, t in (("gate", gate), ("mul", mul), ("add", add)):
+    X_out = X if X_out is None else X_out
+    y_code, out_code = _dtype_code(y), HSA_F32 if out is None else _dtype_code(out)
+    if _bad(X, (M, D), f32t, dev): _refuse(X, "X", (M, D), f32t, dev)
+    if _bad(X_out, (M, D), f32t, dev): _refuse(X_out, "X_out", (M, D), f32t, dev)
+    if _bad(y, (M, D), y.dtype, dev): _refuse(y, "y", (M, D), y.dtype, dev)
+    if out is not None and _bad(out, (M, D), out.dtype, dev): _refuse(out, "out", (M, D), out.dtype, dev)
+    if b is not None and _bad(b, (D,), f32t, dev): _refuse(b, "b", (D,), f32t, dev)
+    if post_g is not None and _bad(post_g, (D,), f32t, dev): _refuse(post_g, "post_g", (D,), f32t, dev)
+    if post_b is not None and _bad(post_b, (D,), f32t, dev): _refuse(post_b, "post_b", (D,), f32t, dev)
+    n_mod = step = None
+    for t in (gate, mul, add):
         if t is None:
             continue
-        if t.dtype != torch.float32 or t.device != X.device or t.dim() not in (1, 2) or t.shape[-1] != D or \
-                t.stride(-1) != 1:
-            raise ValueError(f"{name} must be float32 rows of {D} on X's device")
-        rows, step = (1, D) if t.dim() == 1 else (t.shape[0], t.stride(0) if t.shape[0] > 1 else D)
-        if n_mod is not None and (rows, step) != (n_mod, stride):
+        shape = t.shape
+        rows = 1 if len(shape) == 1 else shape[0]
+        row_step = D if rows == 1 else t.stride(0)
+        if shape[-1] != D or len(shape) > 2 or t.stride(-1) != 1 or t.dtype is not f32t or t.get_device() != dev:
+            raise ValueError(f"gate, mul and add must be float32 rows of {D} on X's device")
+        if n_mod is not None and (rows != n_mod or row_step != step):
             raise ValueError("gate, mul and add must have the same rows and row stride")
-        n_mod, stride = rows, step
-    if mod_row is None and n_mod not in (None, 1):
-        raise ValueError("several modulation rows need mod_row")
-    if mod_row is not None and n_mod is None:
-        raise ValueError("mod_row without gate, mul or add")
+        n_mod, step = rows, row_step
     N = 0
     if mod_row is not None:
-        if mod_row.dim() != 1:
-            raise ValueError("mod_row must be one row number per token")
         N = mod_row.shape[0]
-        _operand(mod_row, "mod_row", (N,), torch.int32)
-    if idx is not None:
-        _operand(idx, "idx", (M,), torch.int32)
-    a = ResidualNormArgsC(_ptr(X), _ptr(X_out), _ptr(y), _ptr(out), _dtype_code(y),
-                          HSA_F32 if out is None else _dtype_code(out), M, D, _ptr(b), _NORMS[post], _NORMS[pre],
-                          _ptr(post_g), _ptr(post_b), _ptr(gate), _ptr(mul), _ptr(add), 1 if modulate else 0,
-                          res_scale, _ptr(mod_row), _ptr(idx), N, n_mod or 1, stride or D)
-    _check(lib().hsa_residual_norm(C.byref(a), _stream(stream)), "hsa_residual_norm")
+        if n_mod is None:
+            raise ValueError("mod_row without gate, mul or add")
+        if _bad(mod_row, (N,), torch.int32, dev): _refuse(mod_row, "mod_row", (N,), torch.int32, dev)
+    elif n_mod not in (None, 1):
+        raise ValueError("several modulation rows need mod_row")
+    if idx is not None and _bad(idx, (M,), torch.int32, dev): _refuse(idx, "idx", (M,), torch.int32, dev)
+    st = _current(dev, stream)
+    a = ResidualNormArgsC(X.data_ptr(), X_out.data_ptr(), y.data_ptr(), _ptr(out), y_code, out_code, M, D, _ptr(b),
+                          _NORMS[post], _NORMS[pre], _ptr(post_g), _ptr(post_b), _ptr(gate), _ptr(mul), _ptr(add),
+                          1 if modulate else 0, res_scale, _ptr(mod_row), _ptr(idx), N, n_mod or 1, step or D)
+    _check(lib().hsa_residual_norm(C.byref(a), st), "hsa_residual_norm")
 
 
 class HostSlot:
