@@ -106,31 +106,55 @@ __global__ void __launch_bounds__(256) k_block_product(const float* __restrict__
 }
 
 // ------------------------------------------------------------------ selection
-// Order key: ascending in the score; 0 = closed, all ones = forced (above +inf, 0xFF800000).
-__device__ __forceinline__ uint32_t route_key(float s, bool forced) {
-  if (forced) return 0xFFFFFFFFu;
-  if (isnan(s)) s = INFINITY;
-  if (s == -INFINITY) return 0u;
-  const uint32_t u = __float_as_uint(s + 0.0f);           // -0 + 0 = +0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+// Order key: ascending in the score; -inf (closed) maps to kRouteClosed, all ones = forced (above +inf,
+// 0xFF800000).  fminf turns NaN into +inf, adding +0 turns -0 into +0.
+constexpr uint32_t kRouteClosed = 0x007FFFFFu;
+__device__ __forceinline__ uint32_t route_key(float s) {
+  const uint32_t u = __float_as_uint(fminf(s, INFINITY) + 0.0f);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 
 constexpr int kRouteMaxBlocks = 16384;
 
+// float of an order key, the largest finite one for keys at or above +inf (interpolation only)
+__device__ __forceinline__ float route_value(uint32_t k) {
+  k = min(k, 0xFF7FFFFFu);
+  return __uint_as_float(k ^ ((uint32_t)((int)~k >> 31) | 0x80000000u));
+}
+
+constexpr int kRouteFew = 32;      // keys a warp ranks against each other to finish the search
+
 // One row of scores per group of W warps (W = 1: 8 rows a block; W = 8: one).  Warp w of the group
-// holds blocks [w 32 V, (w + 1) 32 V) in registers, 32 consecutive ones at a time.  The keep-th largest
-// key is found bit by bit from the highest bit in which the open keys differ, by counting the keys at
-// or above the candidate; the search ends early once exactly `keep` keys are (a distinct cut).  Ties at
-// the cut go to the lowest index.  Then the chosen blocks are written in index order.
+// holds blocks [w 32 V, (w + 1) 32 V) in registers, 32 consecutive ones at a time.
+// The cut is searched between keys lo and hi with count(key >= lo) > keep > count(key >= hi): a pass counts
+// the keys at or above a candidate and replaces one bound, and the search ends when the count is `keep`
+// (a distinct cut) or hi = lo + 1 (ties at lo, given to the lowest index).  Scores are spread smoothly, so
+// the first candidates interpolate between the bounds' values (about 5 passes until 32 of 1182 normal
+// scores are left, against 11 by halving); every third one, and all after the sixth, halve the key
+// interval, which bounds the passes whatever the scores.  Once at most 32 keys are left between the
+// bounds, a warp with many registers of keys moves them to one register a lane and ranks them.
+// Then the chosen blocks are written in index order.  Bound by instructions: a row of 1182 scores
+// takes a warp about 1500, against 4.7 KB read.
 template <int W, int V>
-__global__ void __launch_bounds__(256) k_block_select(const float* __restrict__ scores, int rows, int n_blocks,
-                                                      int keep, const uint8_t* __restrict__ forced,
-                                                      int* __restrict__ list, int* __restrict__ count) {
+__global__ void __launch_bounds__(256, V > 40 ? 1 : V > 16 ? 3 : 4)
+    k_block_select(const float* __restrict__ scores, int rows, int n_blocks, int keep,
+                   const uint8_t* __restrict__ forced, int* __restrict__ list, int* __restrict__ count) {
   pdl_prologue();
   __shared__ uint32_t part[2][3][8];
+  __shared__ uint32_t fbits[W * V];
+  __shared__ __align__(16) uint32_t few[W == 1 && V > 8 ? 8 : 1][kRouteFew];
   int turn = 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = W == 1 ? (int)blockIdx.x * 8 + warp : (int)blockIdx.x;
+  if (forced) {
+    // one bit per block, read by every row of the CTA
+    for (int i = warp; i < W * V; i += 8) {
+      const int b = 32 * i + lane;
+      const uint32_t m = __ballot_sync(0xffffffffu, b < n_blocks && forced[b] != 0);
+      if (lane == 0) fbits[i] = m;
+    }
+    __syncthreads();
+  }
   if (row >= rows) return;
   const int base = W == 1 ? 0 : warp * 32 * V;
   const float* src = scores + (size_t)row * n_blocks;
@@ -138,9 +162,11 @@ __global__ void __launch_bounds__(256) k_block_select(const float* __restrict__ 
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int b = base + 32 * i + lane;
-    key[i] = b < n_blocks ? route_key(src[b], forced && forced[b]) : 0u;
+    key[i] = __float_as_uint(b < n_blocks ? __ldcs(src + b) : -INFINITY);
   }
-  // sum over the group of up to three per-lane counts
+#pragma unroll
+  for (int i = 0; i < V; ++i) key[i] = route_key(__uint_as_float(key[i]));
+  // sum over the group of one count per lane
   auto group_sum = [&](uint32_t x) -> uint32_t {
     x = __reduce_add_sync(0xffffffffu, x);
     if constexpr (W > 1) {
@@ -154,13 +180,26 @@ __global__ void __launch_bounds__(256) k_block_select(const float* __restrict__ 
     }
     return x;
   };
-  uint32_t n_open = 0, hi = 0u, lo = 0xFFFFFFFFu;
+  // bounds of the open scores (a forced block's own score may widen them, which is harmless)
+  uint32_t n_open = 0, n_forced = 0, hi = 0u, lo = 0xFFFFFFFFu;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    n_open += key[i] != 0u;
+    lo = min(lo, key[i] - (kRouteClosed + 1u));           // closed: all ones
     hi = max(hi, key[i]);
-    if (key[i]) lo = min(lo, key[i]);
   }
+  if (forced) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const uint32_t m = fbits[(W == 1 ? 0 : warp * V) + i];
+      if (m) {                                            // the same for the whole warp
+        if ((m >> lane) & 1u) key[i] = 0xFFFFFFFFu;
+        n_forced += __popc(m);
+      }
+    }
+    n_forced = group_sum(lane == 0 ? n_forced : 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) n_open += key[i] > kRouteClosed;
   n_open = group_sum(n_open);
   hi = __reduce_max_sync(0xffffffffu, hi);
   lo = __reduce_min_sync(0xffffffffu, lo);
@@ -178,31 +217,82 @@ __global__ void __launch_bounds__(256) k_block_select(const float* __restrict__ 
       lo = min(lo, p[2][w]);
     }
   }
+  lo += kRouteClosed + 1u;
   const uint32_t want = (uint32_t)keep;
-  uint32_t cut = 1u, ties = 0u;                           // chosen: key > cut - 1, or `ties` of key == cut
+  uint32_t cut = kRouteClosed + 1u, ties = 0u;                           // chosen: key >= cut, or > cut and `ties` of == cut
   bool tied = false;
-  if (n_open > want) {
-    // every open key shares the bits above the highest difference of hi and lo
-    const int top = hi == lo ? -1 : 31 - __clz(hi ^ lo);
-    cut = top < 0 ? hi : hi & ~((2u << top) - 1u);
+  if (n_forced >= want) {
+    cut = 0xFFFFFFFFu;
+    ties = want;
+    tied = true;
+  } else if (n_open > want) {
+    uint32_t n_lo = n_open, n_hi = n_forced;
+    hi += 1u;                                             // above every key that is not forced
     bool exact = false;
-    for (int bit = top; bit >= 0; --bit) {
-      const uint32_t cand = cut | (1u << bit);
+    for (int pass = 0; hi - lo > 1u; ++pass) {
+      if (W == 1 && V > 8 && n_lo - n_hi <= kRouteFew) break;
+      uint32_t cand = lo + ((hi - lo) >> 1);
+      if (pass < 6 && pass % 3 != 2) {
+        // aim a tenth past the target, so that the bound on the larger side moves
+        float f = (float)(n_lo - want) / (float)(n_lo - n_hi);
+        f = f > 0.5f ? fmaxf(0.5f, f - 0.1f) : fminf(0.5f, f + 0.1f);
+        const float a = route_value(lo), b = route_value(hi);
+        cand = min(max(route_key(fmaf(b - a, f, a)), lo + 1u), hi - 1u);
+      }
       uint32_t n = 0;
 #pragma unroll
       for (int i = 0; i < V; ++i) n += key[i] >= cand;
       n = group_sum(n);
-      if (n >= want) cut = cand;
+      if (n >= want) {
+        lo = cand;
+        n_lo = n;
+      } else {
+        hi = cand;
+        n_hi = n;
+      }
       if (n == want) {
         exact = true;
         break;
       }
     }
-    if (!exact) {
-      uint32_t above = 0;
+    if (W == 1 && V > 8 && !exact && hi - lo > 1u) {
+      // the keys in [lo, hi), in any order, one a lane
+      uint32_t c = 0;
 #pragma unroll
-      for (int i = 0; i < V; ++i) above += key[i] > cut;
-      ties = want - group_sum(above);
+      for (int i = 0; i < V; ++i) c += key[i] - lo < hi - lo;
+      uint32_t at = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += t;
+      }
+      at -= c;
+      uint32_t* buf = few[warp];
+      buf[lane] = 0u;                                     // below every key
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (key[i] - lo < hi - lo) buf[at++] = key[i];
+      __syncwarp();
+      // rank of the lane's key among them: the one with fewer than the missing number of keys above it,
+      // and at least as many at or above, is the cut
+      const uint32_t mine = buf[lane], need = want - n_hi;
+      uint32_t above = 0, from = 0;
+#pragma unroll
+      for (int j = 0; j < kRouteFew; j += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(buf + j);
+        above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+        from += (o.x >= mine) + (o.y >= mine) + (o.z >= mine) + (o.w >= mine);
+      }
+      const uint32_t who = __ballot_sync(0xffffffffu, above < need && need <= from);
+      const int first = __ffs(who) - 1;
+      lo = __shfl_sync(0xffffffffu, mine, first);
+      n_hi += __shfl_sync(0xffffffffu, above, first);
+      exact = __shfl_sync(0xffffffffu, from, first) == need;
+    }
+    cut = lo;
+    if (!exact) {                                         // n_hi keys above lo, too few; the rest are lo
+      ties = want - n_hi;
       tied = true;
     }
   }
@@ -231,15 +321,25 @@ __global__ void __launch_bounds__(256) k_block_select(const float* __restrict__ 
     pos += min(tie, ties);
   }
   int* dst = list + (size_t)row * keep;
+  if (tied) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const bool t = tied && key[i] == cut;
-    const uint32_t tm = __ballot_sync(0xffffffffu, t);
-    const bool sel = t ? tie + __popc(tm & below) < ties : (key[i] >= cut && key[i] != 0u);
-    const uint32_t sm = __ballot_sync(0xffffffffu, sel);
-    if (sel) dst[pos + __popc(sm & below)] = base + 32 * i + lane;
-    pos += __popc(sm);
-    tie += __popc(tm);
+    for (int i = 0; i < V; ++i) {
+      const bool t = key[i] == cut;
+      const uint32_t tm = __ballot_sync(0xffffffffu, t);
+      const bool sel = t ? tie + __popc(tm & below) < ties : key[i] > cut;
+      const uint32_t sm = __ballot_sync(0xffffffffu, sel);
+      if (sel) dst[pos + __popc(sm & below)] = base + 32 * i + lane;
+      pos += __popc(sm);
+      tie += __popc(tm);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const bool sel = key[i] >= cut;
+      const uint32_t sm = __ballot_sync(0xffffffffu, sel);
+      if (sel) dst[pos + __popc(sm & below)] = base + 32 * i + lane;
+      pos += __popc(sm);
+    }
   }
   const uint32_t total = min(n_open, want);
   const int group_lane = W == 1 ? lane : (int)threadIdx.x;
