@@ -3,16 +3,31 @@
 //   o = softmax(q K_S^T / sqrt(128)) V_S,   S = the keys of blocks list[h][t][0 .. count[h][t]),
 // 0 for a row whose list is empty.  Blocks are 64 or 128 consecutive cache rows.
 //
-// bf16 kernel: CTA = one (query tile, head) unit, or one range of its list.  The tile
-// schedule is that of the full-context kernel (attn_tc.cu): warp 0 loads tiles by TMA, warp 1 issues
-// the MMAs, warps 2-5 and 6-9 run the softmax of the even and the odd tiles, each parity with its own
-// running max, sum and O accumulator in TMEM.  What differs is where a tile's 128 keys come from: one
-// listed 128-row block (two 64-column boxes) or two listed 64-row blocks (four 64 x 64 boxes), so a
-// finer list costs only more TMA instructions, and the tensor-core shapes stay 128 x 128 x 128.
-// The CTA's part of the list is staged in shared memory as first rows of blocks before the pipeline
-// starts; L stands for "no block" (padding of an odd list, an index outside [0, blocks)), which TMA
-// fills with zeros and the softmax masks to -inf.  The stages' row numbers also tell the softmax which
-// tiles need a mask at all (the ragged last block may stand anywhere in a list).
+// bf16 kernel.  A work unit is one (query tile, head), or one range of its list; lists are short (tens of
+// 128-key tiles), so filling and draining the pipeline per unit is what costs: with a CTA per unit it
+// took 6.3 us beside 0.96 us per tile.  Here the CTAs stay (one per SM) and see one endless
+// stream of tiles, g = 0, 1, 2, ..., in which a unit's first tile follows the last one of the unit before:
+//   warp 2      scheduler: takes the next CTA of the grid that has not started yet (cluster launch control,
+//               so units go to the SM that is free whatever their lists' lengths, without a counter in
+//               memory), reads its count and list, and hands units on through a ring of three slots
+//   warp 0      TMA producer: V_g, then K_{g+2}, of whichever unit they belong to; Q of a unit once the
+//               last QK^T of the one before is done
+//   warp 1      TMEM owner and MMA issuer: for each g  O_b (+)= P_g V_g in two halves of 64 keys, then
+//               S_b = Q K_{g+2}^T, b = g % 2
+//   warps 4-7   softmax of the even tiles of the stream, warps 8-11 of the odd ones, one thread per
+//               query row; the two parities keep their own max, sum and O, merged at a unit's end.  The next
+//               unit's first two QK^T run during that epilogue.
+// V_g and K_{g+2} complete on the barriers that count the softmax warps' P_g, so the MMA warp waits twice
+// per tile.  V has one slot per parity: the producer's arrival on p_full[b] for tile g follows its wait for
+// the slot, which the MMA warp releases after it has waited for both halves of P_{g-2}; so no arrival lands
+// a phase early, whatever the unit boundaries.  The softmax warpgroups take the registers that the control
+// warpgroup gives up (208 + 208 + 88 = 3 x 168 a thread at launch; 56 or 72 for the control warps spill or are 1 % slower).
+// A tile's 128 keys are one listed 128-row block (two 64-column boxes) or two listed 64-row blocks (four
+// 64 x 64 boxes), so a finer list costs only more TMA instructions, and the tensor-core shapes stay
+// 128 x 128 x 128.  A unit's list is staged in shared memory as 16-bit block numbers; kNoBlock stands for
+// "no block" (padding of an odd list, an index outside [0, blocks)), which TMA fills with zeros and the
+// softmax masks to -inf.  The numbers also tell the softmax which tiles need a mask at all (the ragged
+// last block may stand anywhere in a list).
 //
 // Rounding: logits, running max and sum, and O are float32; p is rounded to bf16 for the second
 // product (its sum is taken before the rounding, relative error 2^-9 per term), and O once at the end.
@@ -20,21 +35,34 @@
 
 namespace hsa {
 
-struct SparseShared {
-  uint64_t q_full;
-  uint64_t k_full[2], k_empty[3];
-  uint64_t v_empty[2];
-  uint64_t s_full[2], p_full[2][2], o_done;
-  uint32_t tmem;
-  float xm[2][128], xl[2][128];
-};
-
-constexpr int kSpThreads = 64 + 256;
-constexpr int kSpKSlots = 3, kSpVSlots = 2;
+constexpr int kSpThreads = 384;
+constexpr int kSpKSlots = 3, kSpUnits = 3;
 constexpr uint32_t kSpColS = 0, kSpColO = 256, kSpCols = 512;
-constexpr int kSpTilesBytes = kTileBytes * (1 + kSpKSlots + kSpVSlots);
-constexpr int kSpSmemFixed = kSpTilesBytes + 1024 + (int)sizeof(SparseShared);
-static_assert(kSpSmemFixed + 4 * (HSA_SPARSE_MAX_KEEP + 2) <= 227 * 1024, "the longest list must fit shared memory");
+constexpr uint32_t kNoBlock = 0xFFFFu;
+constexpr int kSpMaxBlocks = 65535;
+constexpr int kSpCtrlRegs = 88, kSpSoftRegs = 208;       // per thread; (88 + 2 * 208) * 128 = 168 * 384
+constexpr int kSpAheadTiles = 8;
+
+struct SparseUnit {
+  int u, nt, slot;      // unit, its tiles (0: the end of the stream), partial-result slot or -1
+};
+struct SparseShared {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[2], k_empty[kSpKSlots];   // k_full: the first two tiles of the stream only
+  uint64_t v_empty[2];
+  uint64_t s_full[2], p_full[2][2], o_done, o_free;
+  uint64_t unit_full[kSpUnits], unit_empty[kSpUnits];
+  uint64_t merge[4];                        // a lane quarter's two softmax warps, at a unit's end
+  uint64_t clc;
+  uint4 clc_answer;
+  SparseUnit unit[kSpUnits];
+  uint32_t tmem;
+  float xm[2][2][128], xl[2][2][128];       // [unit % 2][parity][row]
+};
+constexpr int kSpSmemFixed = kTileBytes * (1 + kSpKSlots + 2) + 1024 + (int)sizeof(SparseShared);
+__host__ __device__ constexpr int sparse_list_stride(int keep) { return (keep + 1 + 7) & ~7; }   // 16-bit entries
+constexpr int sparse_smem(int keep) { return kSpSmemFixed + kSpUnits * 2 * sparse_list_stride(keep); }
+static_assert(sparse_smem(HSA_SPARSE_MAX_KEEP) <= 227 * 1024, "three of the longest lists must fit shared memory");
 
 struct SparseList {
   const int* list;    // [H][QT][keep]
@@ -46,21 +74,76 @@ struct SparseList {
 __device__ __forceinline__ int listed_blocks(const SparseList& s, size_t unit) {
   const int n = s.count[unit];
   if (n < 0 || n > s.keep) {
-    if (threadIdx.x == 0) flag_error(HSA_EINDEX);
+    flag_error(HSA_EINDEX);
     return n < 0 ? 0 : s.keep;
   }
   return n;
 }
 
-// First cache row of each listed block of [first, first + n) into rows[0, n), L for a bad index
-__device__ __forceinline__ void stage_rows(const SparseList& s, size_t unit, int first, int n, int L, int* rows) {
-  const int* src = s.list + unit * s.keep + first;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int b = src[i];
-    const bool ok = b >= 0 && b < s.n_blocks;
-    if (!ok) flag_error(HSA_EINDEX);
-    rows[i] = ok ? b * s.block : L;
+template <int R>
+__device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// Ask for a CTA of this grid that has not started: 16 bytes into `answer`, completing on `bar`
+__device__ __forceinline__ void clc_request(uint4* answer, uint64_t* bar) {
+  mbar_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+               ::"r"(smem_u32(answer)), "r"(smem_u32(bar))
+               : "memory");
+}
+// The CTA's index, or -1 when every CTA has started
+__device__ __forceinline__ int clc_answer_cta(const uint4* answer) {
+  int x = -1;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t.reg .b32 x;\n\t"
+      "ld.shared.b128 r, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "mov.b32 x, 0xFFFFFFFF;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 x, r;\n\t"
+      "mov.b32 %0, x;\n\t}\n"
+      : "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return x;
+}
+
+// A role's position in the ring of units
+struct UnitCursor {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance() {
+    if (++s == kSpUnits) {
+      s = 0;
+      phase ^= 1u;
+    }
   }
+};
+
+// Chunk j of lane 4 q + i  <->  chunk i of lane 4 q + j, i, j < 4
+__device__ __forceinline__ uint4 shfl_xor_u4(uint4 v, int m) {
+  return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m),
+                    __shfl_xor_sync(0xffffffffu, v.z, m), __shfl_xor_sync(0xffffffffu, v.w, m));
+}
+__device__ __forceinline__ void quad_transpose(uint4 (&c)[4], int lane) {
+#pragma unroll
+  for (int m = 1; m <= 2; m <<= 1) {
+    const bool up = (lane & m) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & m) continue;
+      const uint4 got = shfl_xor_u4(up ? c[i] : c[i | m], m);
+      if (up) c[i] = got;
+      else c[i | m] = got;
+    }
+  }
+}
+
+// The whole warp waits and goes on together
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  const bool r = __shfl_sync(0xffffffffu, mbar_wait(bar, parity), 0);
+  __syncwarp();
+  return r;
 }
 
 __global__ void __launch_bounds__(kSpThreads, 1)
@@ -73,59 +156,36 @@ __global__ void __launch_bounds__(kSpThreads, 1)
   uint8_t* sQ = smem;
   uint8_t* sK = smem + kTileBytes;
   uint8_t* sV = sK + kSpKSlots * kTileBytes;
-  SparseShared* sh = reinterpret_cast<SparseShared*>(sV + kSpVSlots * kTileBytes);
-  int* rows = reinterpret_cast<int*>(sh + 1);
+  SparseShared* sh = reinterpret_cast<SparseShared*>(sV + 2 * kTileBytes);
+  uint16_t* lists = reinterpret_cast<uint16_t*>(sh + 1);  // [kSpUnits][stride]
+  const int stride = sparse_list_stride(sl.keep);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int u = blockIdx.x, split = 0, n_split = 1, slot = -1;
-  if (u >= grid.u_full) {
-    const int t = u - grid.u_full;
-    u = grid.u_full + t / grid.s_tail;
-    split = t % grid.s_tail;
-    n_split = grid.s_tail;
-    if (n_split > 1) slot = t;
-  }
-  const int m0 = (u % grid.QT) * kAttnBM, h = u / grid.QT;
   const bool halves = sl.block == 64;                     // two blocks per 128-key tile
-  const int n_list = listed_blocks(sl, (size_t)u);
-  const int nt_all = halves ? (n_list + 1) >> 1 : n_list;
-  const int j0 = (int)((long long)split * nt_all / n_split);
-  const int nt = (int)((long long)(split + 1) * nt_all / n_split) - j0;
-
-  if (nt == 0) {                                          // nothing listed: the rows are 0 (or add nothing)
-    if (slot >= 0) {
-      if (threadIdx.x < kAttnBM) grid.part_ml[(size_t)slot * kAttnBM + threadIdx.x] = make_float2(-INFINITY, 0.f);
-    } else {
-      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-      for (int i = threadIdx.x; i < kAttnBM * 16; i += kSpThreads) {
-        const int r = m0 + (i >> 4);
-        if (r < M) *reinterpret_cast<uint4*>(O + (size_t)r * (H * 128) + h * 128 + (i & 15) * 8) = z;
-      }
-    }
-    return;
-  }
 
   if (threadIdx.x == 0) {
     mbar_init(&sh->q_full, 1);
+    mbar_init(&sh->q_empty, 1);
     for (int s = 0; s < kSpKSlots; ++s) mbar_init(&sh->k_empty[s], 1);
-    for (int s = 0; s < kSpVSlots; ++s) mbar_init(&sh->v_empty[s], 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh->k_full[b], 1);
+      mbar_init(&sh->v_empty[b], 1);
       mbar_init(&sh->s_full[b], 1);
       mbar_init(&sh->p_full[b][0], 129);   // the parity's 128 softmax threads + the producer
       mbar_init(&sh->p_full[b][1], 129);
     }
     mbar_init(&sh->o_done, 1);
+    mbar_init(&sh->o_free, 256);
+    for (int s = 0; s < kSpUnits; ++s) {
+      mbar_init(&sh->unit_full[s], 1);
+      mbar_init(&sh->unit_empty[s], 10);   // producer, MMA issuer, eight softmax warps
+    }
+    for (int q = 0; q < 4; ++q) mbar_init(&sh->merge[q], 64);
+    mbar_init(&sh->clc, 1);
     fence_mbar_init();
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
-  }
-  {
-    const int per = halves ? 2 : 1, first = j0 * per;
-    const int n = min(nt * per, n_list - first);
-    stage_rows(sl, (size_t)u, first, n, L, rows);
-    if (threadIdx.x == 0 && n < nt * per) rows[n] = L;
   }
   if (warp == 1) {
     tmem_alloc(&sh->tmem, kSpCols);
@@ -136,246 +196,449 @@ __global__ void __launch_bounds__(kSpThreads, 1)
   tc_fence_after();
   const uint32_t tm = sh->tmem;
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- TMA producer
-    const int x0 = h * 128;
-    const bool leader = elect_one();
-    // the 128 keys of local tile t, 32 KB completing on `bar`
-    auto load_tile = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int t) {
-      mbar_expect_tx(bar, kTileBytes);
-      if (halves) {
-        const int r0 = rows[2 * t], r1 = rows[2 * t + 1];
-        tma_load_2d(dst, map, bar, x0, r0);
-        tma_load_2d(dst + kTileBytes / 4, map, bar, x0, r1);
-        tma_load_2d(dst + kTileBytes / 2, map, bar, x0 + 64, r0);
-        tma_load_2d(dst + 3 * (kTileBytes / 4), map, bar, x0 + 64, r1);
-      } else {
-        tma_load_2d(dst, map, bar, x0, rows[t]);
-        tma_load_2d(dst + kTileBytes / 2, map, bar, x0 + 64, rows[t]);
-      }
-    };
-    if (leader) {
-      mbar_expect_tx(&sh->q_full, kTileBytes);
-      tma_load_2d(sQ, &tmQ, &sh->q_full, x0, m0);
-      tma_load_2d(sQ + kTileBytes / 2, &tmQ, &sh->q_full, x0 + 64, m0);
-    }
-    auto load_k = [&](int j, uint64_t* bar) -> bool {
-      const int sk = j % kSpKSlots;
-      const bool ok = __shfl_sync(0xffffffffu, mbar_wait(&sh->k_empty[sk], ((j / kSpKSlots) & 1) ^ 1), 0);
-      __syncwarp();
-      if (ok && leader) load_tile(sK + sk * kTileBytes, &tmK, bar, j);
-      return ok;
-    };
-    bool ok = load_k(0, &sh->k_full[0]);
-    if (ok && nt > 1) ok = load_k(1, &sh->k_full[1]);
-    // Phase order of the p_full arrivals: the producer arrives on phase t / 2 of p_full[t % 2][*] only
-    // after waiting for a ring slot that the MMA warp releases after it waited on the previous phase
-    // of the same barrier, so no arrival lands a phase early
-    for (int t = 0; ok && t < nt; ++t) {
-      const int b = t & 1, sv = t % kSpVSlots;
-      ok = __shfl_sync(0xffffffffu, mbar_wait(&sh->v_empty[sv], ((t / kSpVSlots) & 1) ^ 1), 0);
-      __syncwarp();
-      if (!ok) break;
-      if (leader) load_tile(sV + sv * kTileBytes, &tmV, &sh->p_full[b][0], t);
-      if (t + 2 < nt) {
-        ok = load_k(t + 2, &sh->p_full[b][1]);
-      } else {
-        if (leader) mbar_arrive(&sh->p_full[b][1]);
-        __syncwarp();
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
-    constexpr uint32_t idesc_o = idesc_bf16_f32(128, 128, true);
-    const bool leader = elect_one();
-    const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
-    const uint64_t v_desc = sdesc_sw128(smem_u32(sV), kTileBytes / 2, 1024);
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-      const bool r = __shfl_sync(0xffffffffu, mbar_wait(bar, parity), 0);
-      __syncwarp();
-      return r;
-    };
-    auto issue_qk = [&](int t) -> bool {
-      const int sk = t % kSpKSlots, b = t & 1;
-      if (t < 2 && !wait_all(&sh->k_full[t], 0)) return false;
-      tc_fence_after();
-      const uint64_t kd = k_desc + (uint64_t)((sk * kTileBytes) >> 4);
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = ((kk >> 2) * (kTileBytes / 2) + (kk & 3) * 32) >> 4;
-          umma_ss(tm + kSpColS + b * 128, q_desc + off, kd + off, idesc_s, kk > 0);
+  if (warp < 4) {
+    regs_give<kSpCtrlRegs>();
+    if (warp == 2) {
+      // ---------------------------------------------------------------- scheduler
+      UnitCursor at;
+      uint32_t clc_phase = 0;
+      int cta = blockIdx.x, staged = 0, last_nt = 0;
+      bool ok = true;
+      while (true) {
+        int nt = 0, slot = -1, u = -1;
+        if (cta >= 0) {
+          int split = 0, n_split = 1;
+          u = cta;
+          if (u >= grid.u_full) {
+            const int t = u - grid.u_full;
+            u = grid.u_full + t / grid.s_tail;
+            split = t % grid.s_tail;
+            n_split = grid.s_tail;
+            if (n_split > 1) slot = t;
+          }
+          const int n_list = listed_blocks(sl, (size_t)u);
+          const int nt_all = halves ? (n_list + 1) >> 1 : n_list;
+          const int j0 = (int)((long long)split * nt_all / n_split);
+          nt = (int)((long long)(split + 1) * nt_all / n_split) - j0;
+          if (nt > 0 && ok) {
+            // slot free: the unit kSpUnits before it is finished everywhere
+            if (staged >= kSpUnits) ok = warp_wait(&sh->unit_empty[at.s], at.phase ^ 1u);
+            const int per = halves ? 2 : 1, first = j0 * per, n = min(nt * per, n_list - first);
+            const int* src = sl.list + (size_t)u * sl.keep + first;
+            uint16_t* dst = lists + at.s * stride;
+            for (int i = lane; i < nt * per; i += 32) {
+              int b = (int)kNoBlock;
+              if (i < n) {
+                b = src[i];
+                if (b < 0 || b >= sl.n_blocks) {
+                  flag_error(HSA_EINDEX);
+                  b = (int)kNoBlock;
+                }
+              }
+              dst[i] = (uint16_t)b;
+            }
+          } else if (nt == 0) {
+            // nothing listed: the rows are 0 (or this range adds nothing)
+            if (slot >= 0) {
+              for (int r = lane; r < kAttnBM; r += 32)
+                grid.part_ml[(size_t)slot * kAttnBM + r] = make_float2(-INFINITY, 0.f);
+            } else {
+              const int m0 = (u % grid.QT) * kAttnBM, h = u / grid.QT;
+              for (int i = lane; i < kAttnBM * 16; i += 32) {
+                const int r = m0 + (i >> 4);
+                if (r < M)
+                  *reinterpret_cast<uint4*>(O + (size_t)r * (H * 128) + h * 128 + (i & 15) * 8) =
+                      make_uint4(0u, 0u, 0u, 0u);
+              }
+            }
+          }
+        } else if (staged >= kSpUnits && ok) {
+          ok = warp_wait(&sh->unit_empty[at.s], at.phase ^ 1u);
         }
-        umma_commit(&sh->s_full[b]);
-        umma_commit(&sh->k_empty[sk]);
+        if (ok && (nt > 0 || cta < 0)) {
+          if (lane == 0) sh->unit[at.s] = SparseUnit{u, nt, slot};
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->unit_full[at.s]);
+          // one unit ahead is enough when the one just staged is long: taking more would leave other SMs
+          // idle at the end (the unit before it is finished first)
+          const int prev = at.s == 0 ? kSpUnits - 1 : at.s - 1;
+          const uint32_t prev_phase = at.s == 0 ? at.phase ^ 1u : at.phase;
+          at.advance();
+          ++staged;
+          last_nt = nt;
+          if (cta >= 0 && staged >= 2 && last_nt >= kSpAheadTiles) ok = warp_wait(&sh->unit_empty[prev], prev_phase) && ok;
+        }
+        if (cta < 0 || !ok) break;
+        if (lane == 0) clc_request(&sh->clc_answer, &sh->clc);
+        ok = warp_wait(&sh->clc, clc_phase);
+        if (!ok) break;
+        clc_phase ^= 1u;
+        cta = clc_answer_cta(&sh->clc_answer);
+        __syncwarp();
+        if (lane == 0) fence_proxy_async_smem();          // read before the next answer is written
       }
-      __syncwarp();
-      return true;
-    };
-    bool ok = wait_all(&sh->q_full, 0);
-    if (ok) ok = issue_qk(0);
-    if (ok && nt > 1) ok = issue_qk(1);
-    for (int t = 0; ok && t < nt; ++t) {
-      const int b = t & 1, sv = t % kSpVSlots;
-      const uint64_t vd = v_desc + (uint64_t)((sv * kTileBytes) >> 4);
-      bool got = true;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if (!wait_all(&sh->p_full[b][q], (t / 2) & 1)) { got = false; break; }
+    } else if (warp == 0) {
+      // ---------------------------------------------------------------- TMA producer
+      const bool leader = elect_one();
+      // the 128 keys of tile t of the list in ring slot s, 32 KB completing on `bar`
+      auto load_tile = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int s, int t, int x0) {
+        const uint16_t* l = lists + s * stride;
+        mbar_expect_tx(bar, kTileBytes);
+        auto row = [&](uint32_t b) { return b == kNoBlock ? L : (int)b * sl.block; };
+        if (halves) {
+          const int r0 = row(l[2 * t]), r1 = row(l[2 * t + 1]);
+          tma_load_2d(dst, map, bar, x0, r0);
+          tma_load_2d(dst + kTileBytes / 4, map, bar, x0, r1);
+          tma_load_2d(dst + kTileBytes / 2, map, bar, x0 + 64, r0);
+          tma_load_2d(dst + 3 * (kTileBytes / 4), map, bar, x0 + 64, r1);
+        } else {
+          const int r = row(l[t]);
+          tma_load_2d(dst, map, bar, x0, r);
+          tma_load_2d(dst + kTileBytes / 2, map, bar, x0 + 64, r);
+        }
+      };
+      UnitCursor kc, vc;
+      int k_t = 0, k_nt = 0, k_x0 = 0, k_slot = 0, n_q = 0;
+      uint32_t k_phase = 1;
+      bool ok = true, k_end = false, k_first = true;
+      // the stream's next K tile, completing on `bar`; false at the stream's end
+      auto load_k = [&](uint64_t* bar) -> bool {
+        if (k_t == k_nt) {
+          if (!k_first) kc.advance();
+          k_first = false;
+          ok = warp_wait(&sh->unit_full[kc.s], kc.phase);
+          const SparseUnit unit = sh->unit[kc.s];
+          if (!ok || unit.nt == 0) {
+            k_end = true;
+            return false;
+          }
+          k_t = 0;
+          k_nt = unit.nt;
+          k_x0 = unit.u / grid.QT * 128;
+          if (n_q > 0) ok = warp_wait(&sh->q_empty, (n_q - 1) & 1);
+          if (!ok) return false;
+          if (leader) {
+            const int m0 = unit.u % grid.QT * kAttnBM;
+            mbar_expect_tx(&sh->q_full, kTileBytes);
+            tma_load_2d(sQ, &tmQ, &sh->q_full, k_x0, m0);
+            tma_load_2d(sQ + kTileBytes / 2, &tmQ, &sh->q_full, k_x0 + 64, m0);
+          }
+          __syncwarp();
+          ++n_q;
+        }
+        ok = warp_wait(&sh->k_empty[k_slot], k_phase);
+        if (!ok) return false;
+        if (leader) load_tile(sK + k_slot * kTileBytes, &tmK, bar, kc.s, k_t, k_x0);
+        __syncwarp();
+        ++k_t;
+        if (++k_slot == kSpKSlots) {
+          k_slot = 0;
+          k_phase ^= 1u;
+        }
+        return true;
+      };
+      if (load_k(&sh->k_full[0])) load_k(&sh->k_full[1]);
+      uint32_t g = 0;
+      while (ok) {
+        ok = warp_wait(&sh->unit_full[vc.s], vc.phase);
+        if (!ok) break;
+        const int nt = sh->unit[vc.s].nt, x0 = sh->unit[vc.s].u / grid.QT * 128;
+        if (nt == 0) break;
+        for (int t = 0; ok && t < nt; ++t, ++g) {
+          const uint32_t b = g & 1u;
+          ok = warp_wait(&sh->v_empty[b], ((g >> 1) & 1u) ^ 1u);
+          if (!ok) break;
+          if (leader) load_tile(sV + b * kTileBytes, &tmV, &sh->p_full[b][0], vc.s, t, x0);
+          __syncwarp();
+          if (k_end || !load_k(&sh->p_full[b][1])) {
+            if (ok && leader) mbar_arrive(&sh->p_full[b][1]);
+            __syncwarp();
+          }
+        }
+        if (ok && lane == 0) mbar_arrive(&sh->unit_empty[vc.s]);
+        __syncwarp();
+        vc.advance();
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA issuer
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(128, 128, true);
+      const bool leader = elect_one();
+      const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(sV), kTileBytes / 2, 1024);
+      UnitCursor qc, pc;
+      int q_t = 0, q_nt = 0, q_slot = 0, n_q = 0, n_o = 0;
+      bool ok = true, q_end = false, q_first = true;
+      // QK^T of the stream's next tile into S_b; its K has arrived (the first two wait here)
+      auto issue_qk = [&](uint32_t g) -> bool {
+        if (q_t == q_nt) {
+          if (!q_first) qc.advance();
+          q_first = false;
+          ok = warp_wait(&sh->unit_full[qc.s], qc.phase);
+          q_nt = ok ? sh->unit[qc.s].nt : 0;
+          if (q_nt == 0) {
+            q_end = true;
+            return false;
+          }
+          q_t = 0;
+          ok = warp_wait(&sh->q_full, n_q & 1);
+          ++n_q;
+          if (!ok) return false;
+        }
+        if (g < 2) {
+          ok = warp_wait(&sh->k_full[g], 0);
+          if (!ok) return false;
+        }
+        const uint32_t b = g & 1u;
+        ++q_t;
         tc_fence_after();
+        const uint64_t kd = k_desc + (uint64_t)((q_slot * kTileBytes) >> 4);
         if (leader) {
 #pragma unroll
-          for (int kk = q * 4; kk < q * 4 + 4; ++kk)
-            umma_ts(tm + kSpColO + b * 128, tm + kSpColS + b * 128 + kk * 8, vd + (uint64_t)(kk * 2048 >> 4), idesc_o,
-                    (t >= 2 || kk > 0));
-          if (q == 1) umma_commit(&sh->v_empty[sv]);
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = ((kk >> 2) * (kTileBytes / 2) + (kk & 3) * 32) >> 4;
+            umma_ss(tm + kSpColS + b * 128, q_desc + off, kd + off, idesc_s, kk > 0);
+          }
+          umma_commit(&sh->s_full[b]);
+          umma_commit(&sh->k_empty[q_slot]);
+          if (q_t == q_nt) umma_commit(&sh->q_empty);
         }
         __syncwarp();
+        if (++q_slot == kSpKSlots) q_slot = 0;
+        return true;
+      };
+      if (issue_qk(0)) issue_qk(1);
+      uint32_t g = 0;
+      while (ok) {
+        ok = warp_wait(&sh->unit_full[pc.s], pc.phase);
+        if (!ok) break;
+        const int nt = sh->unit[pc.s].nt;
+        if (nt == 0) break;
+        // the first PV of a unit overwrites O: the epilogue of the one before has read it
+        if (n_o > 0) ok = warp_wait(&sh->o_free, (n_o - 1) & 1);
+        for (int t = 0; ok && t < nt; ++t, ++g) {
+          const uint32_t b = g & 1u;
+          const uint64_t vd = v_desc + (uint64_t)((b * kTileBytes) >> 4);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (!ok) break;
+            ok = warp_wait(&sh->p_full[b][q], (g >> 1) & 1u);
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+              for (int kk = q * 4; kk < q * 4 + 4; ++kk)
+                umma_ts(tm + kSpColO + b * 128, tm + kSpColS + b * 128 + kk * 8, vd + (uint64_t)(kk * 2048 >> 4),
+                        idesc_o, (t >= 2 || kk > 0));
+              if (q == 1) umma_commit(&sh->v_empty[b]);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (t == nt - 1) {
+            if (leader) umma_commit(&sh->o_done);
+            __syncwarp();
+          }
+          if (!q_end) issue_qk(g + 2);
+        }
+        ++n_o;
+        if (ok && lane == 0) mbar_arrive(&sh->unit_empty[pc.s]);
+        __syncwarp();
+        pc.advance();
       }
-      if (!got) break;
-      if (t + 2 < nt) ok = issue_qk(t + 2);
     }
-    if (leader) umma_commit(&sh->o_done);
-    __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax warps
+    regs_take<kSpSoftRegs>();
     const int quarter = warp & 3;
-    const int par = (warp - 2) >> 2;
+    const uint32_t par = (warp >> 2) - 1;
     const int row = quarter * 32 + lane;
     const uint32_t lane_base = tm + ((uint32_t)(quarter * 32) << 16);
     const uint32_t s_col = lane_base + kSpColS + par * 128, o_col = lane_base + kSpColO + par * 128;
     const float sc = 0.12751743074680484f;               // log2(e) / sqrt(128)
-    float m = -INFINITY, l = 0.f;
-    for (int t = par; t < nt; t += 2) {
-      // keys of the tile's two 64-key halves that exist (64 or more: all)
-      const int v0 = L - (halves ? rows[2 * t] : rows[t]);
-      const int v1 = halves ? L - rows[2 * t + 1] : v0 - 64;
-      mbar_wait(&sh->s_full[par], (t / 2) & 1);
-      __syncwarp();
-      tc_fence_after();
-      uint32_t sr[128];
+    UnitCursor at;
+    uint32_t s_phase = 0, first = 0, n_unit = 0;          // first: parity of the unit's first tile
+    // The unit whose tiles are done and whose rows are still to be written.  The parity of its last tile
+    // writes at once; the other one, whose next S is ready before that last PV is done, first takes the
+    // softmax of its first tile of the next unit, so that P is there when O comes free.
+    int done_u = -1, done_slot = -1;
+    bool done_two = false;
+    uint32_t done_first = 0, done_last = 0;               // parities of its first and last tile
+    while (warp_wait(&sh->unit_full[at.s], at.phase)) {
+      const int nt = sh->unit[at.s].nt;                   // 0: the end
+      const uint16_t* blk = lists + at.s * stride;
+      float m = -INFINITY, l = 0.f;
+      int t = (int)(par ^ first);
+      bool write = t >= nt || done_last == par;
+      do {
+        if (done_u >= 0 && write) {
+          // -------------------------------------------------------------- merge the parities, write the rows
+          // F: the parity of the unit's first tile, G: the other one, without a tile in a unit of one
+          const uint32_t pb = (n_unit & 1u) ^ 1u;
+          const float(*xm)[128] = sh->xm[pb];
+          const float(*xl)[128] = sh->xl[pb];
+          mbar_wait(&sh->merge[quarter], pb);
+          const float mF = xm[done_first][row], mG = xm[done_first ^ 1u][row];
+          const float mm = fmaxf(mF, mG);
+          const float ms = mm == -INFINITY ? 0.f : mm;    // no key at all: weights 0
+          const float aF = ex2_approx(mF - ms), aG = ex2_approx(mG - ms);
+          const float den = aF * xl[done_first][row] + aG * xl[done_first ^ 1u][row];
+          const float inv_l = den > 0.f ? 1.0f / den : 0.f;
+          const float wF = done_slot >= 0 ? aF : aF * inv_l, wG = done_slot >= 0 ? aG : aG * inv_l;
+          if (done_slot >= 0 && par == 0)
+            grid.part_ml[(size_t)done_slot * kAttnBM + row] = make_float2(mm, den);
+          mbar_wait(&sh->o_done, pb);
+          __syncwarp();
+          tc_fence_after();
+          // this warp writes output columns [64 par, 64 par + 64) of its 32 rows, 32 at a time
+          const int m0 = (done_u % grid.QT) * kAttnBM;
+#pragma unroll 1
+          for (int hc = 0; hc < 2; ++hc) {
+            const uint32_t col = par * 64 + (uint32_t)hc * 32;
+            uint32_t oF[32], oG[32];
+            __syncwarp();
+            tmem_ld32(lane_base + kSpColO + done_first * 128 + col, oF);
+            if (done_two) tmem_ld32(lane_base + kSpColO + (done_first ^ 1u) * 128 + col, oG);
+            tmem_ld_wait();
+            if (hc == 1) {
+              tc_fence_before();
+              mbar_arrive(&sh->o_free);
+            }
+            if (!done_two) {
 #pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4)
-        tmem_ld32(s_col + q4 * 32, *reinterpret_cast<uint32_t(*)[32]>(sr + q4 * 32));
-      tmem_ld_wait();
-      if (v0 < 64 || v1 < 64) {
+              for (int e = 0; e < 32; ++e) oG[e] = 0u;
+            }
+            float f[32];
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          if (c >= v0) sr[c] = __float_as_uint(-INFINITY);
-          if (c >= v1) sr[64 + c] = __float_as_uint(-INFINITY);
+            for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(oF[e]), wF, __uint_as_float(oG[e]) * wG);
+            if (done_slot >= 0) {
+              float* dst = grid.part_o + ((size_t)done_slot * kAttnBM + row) * 128 + col;
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(dst + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+            } else {
+              // 16-byte chunks of 8 channels, transposed among the four lanes of a quad, so that a store
+              // covers 64 consecutive bytes of 8 rows instead of 16 bytes of 32
+              uint4 ch[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                ch[i] = make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]), pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
+                                   pack_bf16x2(f[8 * i + 4], f[8 * i + 5]), pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
+              quad_transpose(ch, lane);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = m0 + quarter * 32 + (lane & ~3) + i;
+                if (r < M)
+                  *reinterpret_cast<uint4*>(O + (size_t)r * (H * 128) + (done_u / grid.QT) * 128 + col +
+                                            (lane & 3) * 8) = ch[i];
+              }
+            }
+          }
+          __syncwarp();
+          done_u = -1;
         }
-      }
-      float mx8[8];
+        write = true;
+        if (t < nt) {
+        // keys of the tile's two 64-key halves that exist (64 or more: all)
+        int v0, v1;
+        {
+          const uint32_t b0 = blk[halves ? 2 * t : t], b1 = halves ? blk[2 * t + 1] : b0;
+          v0 = b0 == kNoBlock ? 0 : L - (int)b0 * sl.block;
+          v1 = b1 == kNoBlock ? 0 : L - (int)b1 * sl.block;
+          if (!halves) v1 -= 64;
+        }
+        mbar_wait(&sh->s_full[par], s_phase);
+        s_phase ^= 1u;
+        __syncwarp();
+        tc_fence_after();
+        uint32_t sr[128];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mx8[e] = __uint_as_float(sr[e]);
+        for (int q4 = 0; q4 < 4; ++q4)
+          tmem_ld32(s_col + q4 * 32, *reinterpret_cast<uint32_t(*)[32]>(sr + q4 * 32));
+        tmem_ld_wait();
+        if (v0 < 64 || v1 < 64) {
 #pragma unroll
-      for (int c = 8; c < 128; c += 2)
-        mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-      const float m_tile = sc * fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                      fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-      // lazy rescale: the max moves only when it grew by more than 2^8
-      bool need = false;
-      float corr = 1.0f;
-      if (t == par) {
-        m = m_tile;
-      } else if (m_tile > m + 8.0f) {
-        need = true;
-        corr = ex2_approx(m - m_tile);
-        l *= corr;
-        m = m_tile;
-      }
-      const bool any_need = __any_sync(0xffffffffu, need);
-      const float neg_m = m == -INFINITY ? 0.f : -m;      // no key so far: every p is 2^-inf = 0
-      const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(neg_m, neg_m);
-      float2 rs4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int c = hh * 64; c < hh * 64 + 64; c += 2) {
-          const float2 x = ffma2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc2, nm2);
-          const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
-          rs4[(c >> 1) & 3] = fadd2(rs4[(c >> 1) & 3], make_float2(p0, p1));
-          pk[(c >> 1) & 31] = pack_bf16x2(p0, p1);
-          if ((c & 31) == 30) tmem_st16(s_col + (c >> 5) * 16, pk + ((c >> 1) & 31) - 15);
-          if (hh == 1 && c == 66 && !any_need) {
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&sh->p_full[par][0]);
+          for (int c = 0; c < 64; ++c) {
+            if (c >= v0) sr[c] = __float_as_uint(-INFINITY);
+            if (c >= v1) sr[64 + c] = __float_as_uint(-INFINITY);
           }
         }
-      }
-      l += ((rs4[0].x + rs4[0].y) + (rs4[1].x + rs4[1].y)) + ((rs4[2].x + rs4[2].y) + (rs4[3].x + rs4[3].y));
-      if (any_need) {
-        // O of this parity holds the PV of its previous tiles, complete: S was written by an MMA issued
-        // after them, and PV of this tile starts only after the p_full arrivals below
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          tmem_ld32(o_col + c * 32, o);
-          tmem_ld_wait();
+        float mx8[8];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-          tmem_st32(o_col + c * 32, o);
+        for (int e = 0; e < 8; ++e) mx8[e] = __uint_as_float(sr[e]);
+#pragma unroll
+        for (int c = 8; c < 128; c += 2)
+          mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+        const float m_tile = sc * fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                        fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+        // lazy rescale: the max moves only when it grew by more than 2^8
+        bool need = false;
+        float corr = 1.0f;
+        if (t < 2) {
+          m = m_tile;
+        } else if (m_tile > m + 8.0f) {
+          need = true;
+          corr = ex2_approx(m - m_tile);
+          l *= corr;
+          m = m_tile;
         }
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      if (any_need) mbar_arrive(&sh->p_full[par][0]);
-      mbar_arrive(&sh->p_full[par][1]);
-    }
-    // ---------------------------------------------------------------- epilogue: merge the parities
-    sh->xm[par][row] = m;
-    sh->xl[par][row] = l;
-    named_bar_sync(1 + quarter, 64);
-    const bool two = nt >= 2;
-    const float m0v = sh->xm[0][row], m1v = sh->xm[1][row];
-    const float mm = two ? fmaxf(m0v, m1v) : m0v;
-    const float ms = mm == -INFINITY ? 0.f : mm;          // no key at all: weights 0
-    const float a0 = ex2_approx(m0v - ms);
-    const float a1 = two ? ex2_approx(m1v - ms) : 0.f;
-    const float den = a0 * sh->xl[0][row] + (two ? a1 * sh->xl[1][row] : 0.f);
-    const float inv_l = den > 0.f ? 1.0f / den : 0.f;
-    const float w0 = slot >= 0 ? a0 : a0 * inv_l, w1 = slot >= 0 ? a1 : a1 * inv_l;
-    mbar_wait(&sh->o_done, 0);
-    __syncwarp();
-    tc_fence_after();
-    const int grow = m0 + row;
-    if (slot >= 0 && par == 0) grid.part_ml[(size_t)slot * kAttnBM + row] = make_float2(mm, den);
+        const bool any_need = __any_sync(0xffffffffu, need);
+        const float neg_m = m == -INFINITY ? 0.f : -m;    // no key so far: every p is 2^-inf = 0
+        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(neg_m, neg_m);
+        float2 rs4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = hh * 64; c < hh * 64 + 64; c += 2) {
+            const float2 x = ffma2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sc2, nm2);
+            const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+            rs4[(c >> 1) & 3] = fadd2(rs4[(c >> 1) & 3], make_float2(p0, p1));
+            pk[(c >> 1) & 31] = pack_bf16x2(p0, p1);
+            if ((c & 31) == 30) tmem_st16(s_col + (c >> 5) * 16, pk + ((c >> 1) & 31) - 15);
+            if (hh == 1 && c == 66 && !any_need) {
+              tmem_st_wait();
+              tc_fence_before();
+              mbar_arrive(&sh->p_full[par][0]);
+            }
+          }
+        }
+        l += ((rs4[0].x + rs4[0].y) + (rs4[1].x + rs4[1].y)) + ((rs4[2].x + rs4[2].y) + (rs4[3].x + rs4[3].y));
+        if (any_need) {
+          // O of this parity holds the PV of the unit's earlier tiles, complete: S was written by an MMA
+          // issued after them, and PV of this tile starts only after the p_full arrivals below
 #pragma unroll 1
-    for (int c = 0; c < 2; ++c) {
-      const uint32_t col = (uint32_t)(par * 64 + c * 32);
-      uint32_t o0[32], o1[32];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_col + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+            tmem_st32(o_col + c * 32, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        if (any_need) mbar_arrive(&sh->p_full[par][0]);
+        mbar_arrive(&sh->p_full[par][1]);
+        }
+        t += 2;
+      } while (t < nt || done_u >= 0);
+      if (nt == 0) break;
+      done_u = sh->unit[at.s].u;
+      done_slot = sh->unit[at.s].slot;
+      done_two = nt >= 2;
+      done_first = first;
+      done_last = first ^ ((uint32_t)(nt - 1) & 1u);
       __syncwarp();
-      tmem_ld32(lane_base + kSpColO + col, o0);
-      if (two) tmem_ld32(lane_base + kSpColO + 128 + col, o1);
-      tmem_ld_wait();
-      if (!two) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o1[e] = 0u;
-      }
-      float f[32];
-#pragma unroll
-      for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o0[e]), w0, __uint_as_float(o1[e]) * w1);
-      if (slot >= 0) {
-        float* dst = grid.part_o + ((size_t)slot * kAttnBM + row) * 128 + col;
-#pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<float4*>(dst + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
-      } else if (grow < M) {
-        __nv_bfloat16* dst = O + (size_t)grow * (H * 128) + h * 128 + col;
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          uint4 pk4;
-          pk4.x = pack_bf16x2(f[e], f[e + 1]);
-          pk4.y = pack_bf16x2(f[e + 2], f[e + 3]);
-          pk4.z = pack_bf16x2(f[e + 4], f[e + 5]);
-          pk4.w = pack_bf16x2(f[e + 6], f[e + 7]);
-          *reinterpret_cast<uint4*>(dst + e) = pk4;
-        }
-      }
+      if (lane == 0) mbar_arrive(&sh->unit_empty[at.s]);  // done with the list
+      sh->xm[n_unit & 1][par][row] = m;
+      sh->xl[n_unit & 1][par][row] = l;
+      mbar_arrive(&sh->merge[quarter]);
+      first ^= (uint32_t)nt & 1u;
+      ++n_unit;
+      at.advance();
     }
   }
 
@@ -419,6 +682,17 @@ __global__ void __launch_bounds__(256) k_attn_sparse_combine(const float* __rest
 }
 
 // ------------------------------------------------------------------ float32, CUDA cores
+// First cache row of each listed block of [first, first + n) into rows[0, n), L for a bad index
+__device__ __forceinline__ void stage_rows(const SparseList& s, size_t unit, int first, int n, int L, int* rows) {
+  const int* src = s.list + unit * s.keep + first;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int b = src[i];
+    const bool ok = b >= 0 && b < s.n_blocks;
+    if (!ok) flag_error(HSA_EINDEX);
+    rows[i] = ok ? b * s.block : L;
+  }
+}
+
 // The full-context fp32 kernel's tiling (k_attn_f32: 32 query rows per CTA, 64-key tiles) over the list
 // of the rows' query tile; a 128-row block is two tiles.
 __global__ void __launch_bounds__(256, 2)
@@ -598,7 +872,7 @@ int sparse_bf16(const void* Q, int M, const void* K, const void* V, int L, int H
   static PerContextOnce attr;
   rc = attr.ensure([](void**) {
     if (cudaFuncSetAttribute(k_attn_sparse, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSpSmemFixed + 4 * (HSA_SPARSE_MAX_KEEP + 2)) != cudaSuccess)
+                             sparse_smem(HSA_SPARSE_MAX_KEEP)) != cudaSuccess)
       return check_launch("sparse attention: shared-memory attribute");
     return (int)HSA_OK;
   });
@@ -614,8 +888,8 @@ int sparse_bf16(const void* Q, int M, const void* K, const void* V, int L, int H
     g.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + align256(slots * 128 * sizeof(float)));
   }
   ScopedTiming timing(HSA_KCLASS_ATTENTION, st);
-  launch(k_attn_sparse, (unsigned)(ts.u_full + ts.n_tail * ts.s_tail), kSpThreads, kSpSmemFixed + 4 * (sl.keep + 2), st,
-         tq, tk, tv, M, L, H, reinterpret_cast<__nv_bfloat16*>(O), g, sl);
+  launch(k_attn_sparse, (unsigned)(ts.u_full + ts.n_tail * ts.s_tail), kSpThreads, sparse_smem(sl.keep), st, tq,
+          tk, tv, M, L, H, reinterpret_cast<__nv_bfloat16*>(O), g, sl);
   count_launch(1);
   rc = check_launch("sparse attention launch");
   if (rc || ts.s_tail == 1) return rc;
@@ -674,6 +948,8 @@ extern "C" int hsa_sparse_attention(const void* d_q, int M, const void* d_k, con
   if (block_k != 64 && block_k != 128) return set_error(HSA_EINVAL, "sparse_attention: need block_k = 64 or 128");
   if (keep < 1 || keep > HSA_SPARSE_MAX_KEEP)
     return set_error(HSA_EINVAL, "sparse_attention: need 1 <= keep <= 4096");
+  if ((L - 1) / block_k >= kSpMaxBlocks)
+    return set_error(HSA_EINVAL, "sparse_attention: more than 65535 blocks");
   if (M == 0) return HSA_OK;
   if (!d_q || !d_k || !d_v || !d_o || !d_list || !d_count || !aligned16(d_q) || !aligned16(d_k) || !aligned16(d_v) ||
       !aligned16(d_o) || (d_ws && !aligned16(d_ws)))
