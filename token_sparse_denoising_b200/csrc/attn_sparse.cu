@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
         }
       };
       UnitCursor kc, vc;
-      int k_t = 0, k_nt = 0, k_x0 = 0, k_slot = 0, n_q = 0;
+      int k_t = 0, k_nt = 0, k_x0 = 0, k_m0 = 0, k_slot = 0, n_q = 0;
       uint32_t k_phase = 1;
       bool ok = true, k_end = false, k_first = true;
       // the stream's next K tile, completing on `bar`; false at the stream's end
@@ -315,16 +315,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
           k_t = 0;
           k_nt = unit.nt;
           k_x0 = unit.u / grid.QT * 128;
-          if (n_q > 0) ok = warp_wait(&sh->q_empty, (n_q - 1) & 1);
-          if (!ok) return false;
-          if (leader) {
-            const int m0 = unit.u % grid.QT * kAttnBM;
-            mbar_expect_tx(&sh->q_full, kTileBytes);
-            tma_load_2d(sQ, &tmQ, &sh->q_full, k_x0, m0);
-            tma_load_2d(sQ + kTileBytes / 2, &tmQ, &sh->q_full, k_x0 + 64, m0);
-          }
-          __syncwarp();
-          ++n_q;
+          k_m0 = unit.u % grid.QT * kAttnBM;
         }
         ok = warp_wait(&sh->k_empty[k_slot], k_phase);
         if (!ok) return false;
@@ -334,6 +325,18 @@ __global__ void __launch_bounds__(kSpThreads, 1)
         if (++k_slot == kSpKSlots) {
           k_slot = 0;
           k_phase ^= 1u;
+        }
+        if (k_t == 1) {
+          // a unit's Q follows its first K: the buffer is free once the last QK^T of the unit before is done,
+          // and that wait must not hold up the P barrier that this K completes on
+          if (n_q > 0) ok = warp_wait(&sh->q_empty, (n_q - 1) & 1);
+          if (ok && leader) {
+            mbar_expect_tx(&sh->q_full, kTileBytes);
+            tma_load_2d(sQ, &tmQ, &sh->q_full, k_x0, k_m0);
+            tma_load_2d(sQ + kTileBytes / 2, &tmQ, &sh->q_full, k_x0 + 64, k_m0);
+          }
+          __syncwarp();
+          ++n_q;
         }
         return true;
       };
@@ -493,11 +496,11 @@ __global__ void __launch_bounds__(kSpThreads, 1)
           tc_fence_after();
           // this warp writes output columns [64 par, 64 par + 64) of its 32 rows, 32 at a time
           const int m0 = (done_u % grid.QT) * kAttnBM;
-#pragma unroll 1
+          uint4 ch[2][4];                                 // the row's 64 columns in bf16, chunks of 8
+#pragma unroll
           for (int hc = 0; hc < 2; ++hc) {
             const uint32_t col = par * 64 + (uint32_t)hc * 32;
             uint32_t oF[32], oG[32];
-            __syncwarp();
             tmem_ld32(lane_base + kSpColO + done_first * 128 + col, oF);
             if (done_two) tmem_ld32(lane_base + kSpColO + (done_first ^ 1u) * 128 + col, oG);
             tmem_ld_wait();
@@ -505,34 +508,34 @@ __global__ void __launch_bounds__(kSpThreads, 1)
               tc_fence_before();
               mbar_arrive(&sh->o_free);
             }
-            if (!done_two) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) oG[e] = 0u;
-            }
             float f[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(oF[e]), wF, __uint_as_float(oG[e]) * wG);
+            for (int e = 0; e < 32; ++e) {
+              const float g = done_two ? __uint_as_float(oG[e]) : 0.f;
+              f[e] = fmaf(__uint_as_float(oF[e]), wF, g * wG);
+            }
             if (done_slot >= 0) {
               float* dst = grid.part_o + ((size_t)done_slot * kAttnBM + row) * 128 + col;
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
                 *reinterpret_cast<float4*>(dst + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
-            } else {
-              // 16-byte chunks of 8 channels, transposed among the four lanes of a quad, so that a store
-              // covers 64 consecutive bytes of 8 rows instead of 16 bytes of 32
-              uint4 ch[4];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              ch[hc][i] = make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]), pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
+                                     pack_bf16x2(f[8 * i + 4], f[8 * i + 5]), pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
+          }
+          if (done_slot < 0) {
+            // chunks transposed among the four lanes of a quad, so that a store covers 64 consecutive
+            // bytes of 8 rows instead of 16 bytes of 32
+            const int r0 = m0 + quarter * 32 + (lane & ~3);
+            __nv_bfloat16* dst = O + (size_t)r0 * (H * 128) + (done_u / grid.QT) * 128 + par * 64 + (lane & 3) * 8;
+#pragma unroll
+            for (int hc = 0; hc < 2; ++hc) {
+              quad_transpose(ch[hc], lane);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                ch[i] = make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]), pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
-                                   pack_bf16x2(f[8 * i + 4], f[8 * i + 5]), pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
-              quad_transpose(ch, lane);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int r = m0 + quarter * 32 + (lane & ~3) + i;
-                if (r < M)
-                  *reinterpret_cast<uint4*>(O + (size_t)r * (H * 128) + (done_u / grid.QT) * 128 + col +
-                                            (lane & 3) * 8) = ch[i];
-              }
+                if (r0 + i < M) *reinterpret_cast<uint4*>(dst + (size_t)i * (H * 128) + hc * 32) = ch[hc][i];
             }
           }
           __syncwarp();
