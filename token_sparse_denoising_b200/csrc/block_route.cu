@@ -10,98 +10,316 @@
 // Selection.  Total order of a row's blocks: (score descending, index ascending), scores compared as
 // float32 with -0 equal to 0 and NaN as +inf; -inf closes a block, forced blocks come first.  The
 // result is unique, so it does not depend on how the kernel finds it.
-#include "common.cuh"
+#include "tcgen05.cuh"
 
 namespace hsa {
 
 constexpr int kRouteTile = HSA_QUERY_TILE;
 
-// Mean rows: CTA = one head of one block of rows; 16 threads cover the head's 128 channels, 16 row
-// groups walk the block's rows, joined by a shuffle and through shared memory.  Blocks [0, T) are the
-// query tiles, [T, T + B) the key blocks.  Sums in float32 (at most 128 terms).
-template <typename T>
-__global__ void __launch_bounds__(256) k_block_means(const T* __restrict__ q, int M, const T* __restrict__ k, int L,
-                                                     int H, int block_k, int n_tiles, float* __restrict__ means) {
-  pdl_prologue();
-  __shared__ float part[8][128];
-  const int h = blockIdx.x, j = blockIdx.y;
-  const bool key = j >= n_tiles;
-  const int size = key ? block_k : kRouteTile;
-  const int r0 = (key ? j - n_tiles : j) * size;
-  const int n = min(size, (key ? L : M) - r0);
-  const size_t D = (size_t)H * 128;
-  const int c = (threadIdx.x & 15) * 8, g = threadIdx.x >> 4;
-  const T* src = (key ? k : q) + (size_t)r0 * D + h * 128 + c;
-  float s[8] = {};
-#pragma unroll 8
-  for (int i = 0; i < 8; ++i) {
-    const int r = g + 16 * i;
-    if (r < n) {
-      float v[8];
-      load8(src + (size_t)r * D, v);
+// 8 bf16 values as floats
+__device__ __forceinline__ void widen8(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] += v[e];
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) s[e] += __shfl_xor_sync(0xffffffffu, s[e], 16);
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 16) == 0) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) part[warp][c + e] = s[e];
-  }
-  __syncthreads();
-  if (threadIdx.x < 128) {
-    float t = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) t += part[w][threadIdx.x];
-    means[(size_t)j * D + h * 128 + threadIdx.x] = t / (float)n;
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
   }
 }
 
-// scores[h] = Qm[h] Km[h]^T / sqrt(128) in float32: 64 x 64 tile per CTA, 4 x 4 per thread.
-__global__ void __launch_bounds__(256) k_block_product(const float* __restrict__ means, int n_tiles, int n_blocks,
-                                                       int H, float* __restrict__ scores) {
+// Mean rows.  Bound by the one read of Q and K, so the reads are TMA boxes of 64 rows x 512 bytes through a
+// ring of six slots, one CTA per SM, 192 KB in flight.  An item is one block of rows x 512 bytes of columns,
+// one or two boxes; the SMs walk the items side by side, so rows are read whole.  Warp 8 issues the loads;
+// warps 0-7 take every eighth row of a box, 16 bytes of columns a lane, and leave their sums in shared
+// memory; warps 9-10 join them and write the means while the next item is summed.  (Joined by the summing
+// warps behind a barrier, every item cost them its latency: 84 against 7x us for 40950 rows of 5120 in blocks
+// of 64; plain loads with eight in flight per warp: 42 us for 65520 rows of 1536, this 3x, a bare TMA read
+// without sums 33.)  Rows and columns beyond the matrix arrive as zeros.  Items [0, T) x columns are the
+// query tiles, then the key blocks.  Sums in float32 (at most 128 terms).
+constexpr int kMeanSlots = 6, kMeanBox = 64 * 512, kMeanParts = 3;
+constexpr int kMeanThreads = 11 * 32;
+struct MeanShared {
+  uint64_t full[kMeanSlots], empty[kMeanSlots], part_full[kMeanParts], part_empty[kMeanParts];
+  float part[kMeanParts][8][256];
+};
+constexpr int kMeanSmem = kMeanSlots * kMeanBox + 128 + (int)sizeof(MeanShared);
+
+template <typename T>
+__global__ void __launch_bounds__(kMeanThreads, 1)
+    k_block_means(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, int M, int L, int D,
+                  int block_k, int n_tiles, int n_blocks, int n_items, int cols, __nv_bfloat16* __restrict__ means) {
   pdl_prologue();
-  __shared__ float Qs[32][68], Ks[32][68];
-  const int h = blockIdx.z, t0 = blockIdx.y * 64, b0 = blockIdx.x * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const size_t D = (size_t)H * 128;
-  const float* qm = means + h * 128;
-  const float* km = means + (size_t)n_tiles * D + h * 128;
-  float acc[4][4] = {};
-  for (int c0 = 0; c0 < 128; c0 += 32) {
-    for (int i = threadIdx.x; i < 64 * 8; i += 256) {
-      const int row = i >> 3, c4 = (i & 7) * 4;
-      const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-      const float4 a = t0 + row < n_tiles ? ld4(qm + (size_t)(t0 + row) * D + c0 + c4) : z;
-      const float4 b = b0 + row < n_blocks ? ld4(km + (size_t)(b0 + row) * D + c0 + c4) : z;
-      Qs[c4][row] = a.x; Qs[c4 + 1][row] = a.y; Qs[c4 + 2][row] = a.z; Qs[c4 + 3][row] = a.w;
-      Ks[c4][row] = b.x; Ks[c4 + 1][row] = b.y; Ks[c4 + 2][row] = b.z; Ks[c4 + 3][row] = b.w;
+  constexpr int V = 16 / (int)sizeof(T);                  // columns a lane
+  extern __shared__ uint8_t mean_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(mean_raw) + 127) & ~uintptr_t(127));
+  MeanShared* sh = reinterpret_cast<MeanShared*>(ring + kMeanSlots * kMeanBox);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMeanSlots; ++s) {
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], 8);
     }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      const float4 a = *reinterpret_cast<const float4*>(&Qs[c][ty * 4]);
-      const float4 b = *reinterpret_cast<const float4*>(&Ks[c][tx * 4]);
-      const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+    for (int s = 0; s < kMeanParts; ++s) {
+      mbar_init(&sh->part_full[s], 8);
+      mbar_init(&sh->part_empty[s], 2);
     }
-    __syncthreads();
+    fence_mbar_init();
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
   }
-  const float scale = 0.08838834764831845f;              // 1 / sqrt(128)
+  __syncthreads();
+  int s = 0, ps = 0;
+  uint32_t phase = 0, pphase = 0;
+  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+    const int j = item / cols, x = (item - j * cols) * 32 * V;
+    const bool key = j >= n_tiles;
+    const int size = key ? block_k : kRouteTile;
+    const int r0 = (key ? j - n_tiles : j) * size;
+    const int n = min(size, (key ? L : M) - r0);
+    const int boxes = (n + 63) >> 6;
+    if (warp == 8) {
+      for (int b = 0; b < boxes; ++b) {
+        const bool ok = __shfl_sync(0xffffffffu, mbar_wait(&sh->empty[s], phase ^ 1u), 0);
+        __syncwarp();
+        if (ok && lane == 0) {
+          mbar_expect_tx(&sh->full[s], kMeanBox);
+          tma_load_2d(ring + s * kMeanBox, key ? &tmK : &tmQ, &sh->full[s], x, r0 + 64 * b);
+        }
+        __syncwarp();
+        if (++s == kMeanSlots) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+    } else if (warp < 8) {
+      float sum[V] = {};
+      for (int b = 0; b < boxes; ++b) {
+        mbar_wait(&sh->full[s], phase);
+        __syncwarp();
+        const uint8_t* box = ring + s * kMeanBox + warp * 512 + lane * 16;
+        uint4 raw[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + ty * 4 + i;
-    if (t >= n_tiles) continue;
+        for (int i = 0; i < 8; ++i) raw[i] = *reinterpret_cast<const uint4*>(box + i * 8 * 512);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int b = b0 + tx * 4 + j;
-      if (b < n_blocks) scores[((size_t)h * n_tiles + t) * n_blocks + b] = acc[i][j] * scale;
+        for (int i = 0; i < 8; ++i) {
+          float v[V];
+          if constexpr (V == 8) {
+            widen8(raw[i], v);
+          } else {
+            v[0] = __uint_as_float(raw[i].x); v[1] = __uint_as_float(raw[i].y);
+            v[2] = __uint_as_float(raw[i].z); v[3] = __uint_as_float(raw[i].w);
+          }
+#pragma unroll
+          for (int e = 0; e < V; ++e) sum[e] += v[e];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->empty[s]);
+        if (++s == kMeanSlots) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+      mbar_wait(&sh->part_empty[ps], pphase ^ 1u);
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < V; e += 4)
+        st4(&sh->part[ps][warp][lane * V + e], make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->part_full[ps]);
+    } else {
+      mbar_wait(&sh->part_full[ps], pphase);
+      __syncwarp();
+      const int c = ((warp - 9) * 32 + lane) * 4;
+      if (c < 32 * V) {
+        float4 t = ld4(&sh->part[ps][0][c]);
+#pragma unroll
+        for (int w = 1; w < 8; ++w) {
+          const float4 o = ld4(&sh->part[ps][w][c]);
+          t = make_float4(t.x + o.x, t.y + o.y, t.z + o.z, t.w + o.w);
+        }
+        if (x + c < D) {
+          // the mean as three bf16 terms, each the rounding of what the ones before leave (exact differences)
+          const float cnt = (float)n;
+          t = make_float4(t.x / cnt, t.y / cnt, t.z / cnt, t.w / cnt);
+          const size_t plane = (size_t)(n_tiles + n_blocks) * D;
+          __nv_bfloat16* dst = means + (size_t)j * D + x + c;
+#pragma unroll
+          for (int p = 0; p < 3; ++p) {
+            uint2 u;
+            u.x = pack_bf16x2(t.x, t.y);
+            u.y = pack_bf16x2(t.z, t.w);
+            *reinterpret_cast<uint2*>(dst + p * plane) = u;
+            const float4 r = widen4(u);
+            t = make_float4(t.x - r.x, t.y - r.y, t.z - r.z, t.w - r.w);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->part_empty[ps]);
     }
+    if (++ps == kMeanParts) {
+      ps = 0;
+      pphase ^= 1u;
+    }
+  }
+}
+
+template <typename T>
+static int launch_means(const void* q, int M, const void* k, int L, int H, int block_k, int n_tiles, int n_blocks,
+                        __nv_bfloat16* means, cudaStream_t st) {
+  constexpr bool bf = sizeof(T) == 2;
+  const int D = H * 128, box_cols = 512 / (int)sizeof(T);
+  CUtensorMap tq, tk;
+  int rc = make_tmap_2d(&tq, q, bf, (uint64_t)D, (uint64_t)M, (uint64_t)D * sizeof(T), (uint32_t)box_cols, 64, false);
+  if (!rc)
+    rc = make_tmap_2d(&tk, k, bf, (uint64_t)D, (uint64_t)L, (uint64_t)D * sizeof(T), (uint32_t)box_cols, 64, false);
+  if (rc) return rc;
+  static PerContextOnce attr;
+  rc = attr.ensure([](void**) {
+    if (cudaFuncSetAttribute(k_block_means<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMeanSmem) != cudaSuccess)
+      return check_launch("block_scores: shared-memory attribute");
+    return (int)HSA_OK;
+  });
+  if (rc) return rc;
+  const int cols = (D + box_cols - 1) / box_cols, items = cols * (n_tiles + n_blocks);
+  launch(k_block_means<T>, (unsigned)(items < num_sms() ? items : num_sms()), kMeanThreads, kMeanSmem, st, tq, tk, M, L,
+         D, block_k, n_tiles, n_blocks, items, cols, means);
+  return HSA_OK;
+}
+
+// scores[h] = Qm[h] Km[h]^T / sqrt(128) on the tensor cores, with float32 accuracy: a mean x is kept as three
+// bf16 terms, x = x0 + x1 + x2 with |x1| <= 2^-8 |x| and |x2| <= 2^-16 |x|, and the product takes the six
+// pairs (i, j) with i + j <= 2; what is left out is below 2^-22 of the magnitudes.  A CUDA-core product
+// (8 x 8 values a thread) took 12-19 us for the same sizes, and more with T x B.  CTA = 128 query tiles of a
+// head against a range of its 64-block tiles: the three terms of the query side stay in shared memory, warp
+// 0 loads the block tiles' terms (two buffers of 48 KB), warp 1 issues 48 MMAs a tile into one of two
+// 64-column accumulators, warps 2-5 stage the other one in shared memory and write whole rows.
+// A mean that is not finite gives NaN.
+constexpr int kProdB = 3 * 64 * 128 * 2;                  // one block tile, three terms
+constexpr int kProdStage = 32 * 65 * 4;                   // per epilogue warp
+constexpr int kProdSmem = 3 * kTileBytes + 2 * kProdB + 4 * kProdStage + 1024;
+__global__ void __launch_bounds__(192, 1)
+    k_block_product(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, int n_tiles,
+                    int n_blocks, float* __restrict__ scores) {
+  pdl_prologue();
+  extern __shared__ uint8_t prod_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(prod_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sB = smem + 3 * kTileBytes;
+  __shared__ uint64_t a_full, b_full[2], b_empty[2], d_full[2], d_empty[2];
+  __shared__ uint32_t tmem;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.z, t0 = blockIdx.y * 128;
+  const int nb = (n_blocks + 63) >> 6;
+  const int j0 = (int)((long long)blockIdx.x * nb / gridDim.x);
+  const int nj = (int)((long long)(blockIdx.x + 1) * nb / gridDim.x) - j0;
+  if (threadIdx.x == 0) {
+    mbar_init(&a_full, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&b_full[b], 1);
+      mbar_init(&b_empty[b], 1);
+      mbar_init(&d_full[b], 1);
+      mbar_init(&d_empty[b], 128);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem, 128);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = tmem;
+  if (warp == 0) {
+    const bool leader = elect_one();
+    const int rows = n_tiles + n_blocks, x = h * 128;
+    if (leader) {
+      mbar_expect_tx(&a_full, 3 * kTileBytes);
+      for (int p = 0; p < 3; ++p)
+        for (int c = 0; c < 2; ++c)
+          tma_load_2d(smem + p * kTileBytes + c * (kTileBytes / 2), &tmA, &a_full, x + 64 * c, p * rows + t0);
+    }
+    __syncwarp();
+    for (int i = 0; i < nj; ++i) {
+      const int b = i & 1;
+      const bool ok = __shfl_sync(0xffffffffu, mbar_wait(&b_empty[b], ((i >> 1) & 1) ^ 1), 0);
+      __syncwarp();
+      if (ok && leader) {
+        mbar_expect_tx(&b_full[b], kProdB);
+        for (int p = 0; p < 3; ++p)
+          for (int c = 0; c < 2; ++c)
+            tma_load_2d(sB + b * kProdB + p * (kProdB / 3) + c * (kProdB / 6), &tmB, &b_full[b], x + 64 * c,
+                        p * rows + n_tiles + (j0 + i) * 64);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 1) {
+    const bool leader = elect_one();
+    constexpr uint32_t idesc = idesc_bf16_f32(128, 64, false);
+    const uint64_t ad = sdesc_sw128(smem_u32(smem), 16, 1024), bd = sdesc_sw128(smem_u32(sB), 16, 1024);
+    bool ok = __shfl_sync(0xffffffffu, mbar_wait(&a_full, 0), 0);
+    for (int i = 0; ok && i < nj; ++i) {
+      const int b = i & 1;
+      ok = __shfl_sync(0xffffffffu, mbar_wait(&b_full[b], (i >> 1) & 1), 0);
+      if (ok) ok = __shfl_sync(0xffffffffu, mbar_wait(&d_empty[b], ((i >> 1) & 1) ^ 1), 0);
+      __syncwarp();
+      if (!ok) break;
+      tc_fence_after();
+      if (leader) {
+        // smallest pairs first: (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
+#pragma unroll
+        for (int e = 0; e < 6; ++e) {
+          constexpr int kP[6] = {2, 1, 0, 1, 0, 0}, kR[6] = {0, 1, 2, 0, 1, 0};
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ss(tm + b * 64,
+                    ad + (uint64_t)((kP[e] * kTileBytes + (kk >> 2) * (kTileBytes / 2) + (kk & 3) * 32) >> 4),
+                    bd + (uint64_t)((b * kProdB + kR[e] * (kProdB / 3) + (kk >> 2) * (kProdB / 6) + (kk & 3) * 32) >> 4),
+                    idesc, e > 0 || kk > 0);
+        }
+        umma_commit(&d_full[b]);
+        umma_commit(&b_empty[b]);
+      }
+      __syncwarp();
+    }
+  } else {
+    // thread = row of the tile; rows staged 65 floats apart, free of bank conflicts in both directions
+    const int quarter = warp & 3;
+    const float scale = 0.08838834764831845f;            // 1 / sqrt(128)
+    float* stage = reinterpret_cast<float*>(sB + 2 * kProdB + quarter * kProdStage);
+    const int rows = min(32, n_tiles - t0 - quarter * 32);
+    for (int i = 0; i < nj; ++i) {
+      const int b = i & 1, b0 = (j0 + i) * 64;
+      mbar_wait(&d_full[b], (i >> 1) & 1);
+      __syncwarp();
+      tc_fence_after();
+      uint32_t v[64];
+      tmem_ld32(tm + ((uint32_t)(quarter * 32) << 16) + b * 64, *reinterpret_cast<uint32_t(*)[32]>(v));
+      tmem_ld32(tm + ((uint32_t)(quarter * 32) << 16) + b * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(&d_empty[b]);
+#pragma unroll
+      for (int e = 0; e < 64; ++e) stage[lane * 65 + e] = __uint_as_float(v[e]) * scale;
+      __syncwarp();
+      float* dst = scores + ((size_t)h * n_tiles + t0 + quarter * 32) * n_blocks + b0;
+      const bool in0 = b0 + lane < n_blocks, in1 = b0 + 32 + lane < n_blocks;
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) {
+        if (in0) dst[(size_t)r * n_blocks + lane] = stage[r * 65 + lane];
+        if (in1) dst[(size_t)r * n_blocks + 32 + lane] = stage[r * 65 + 32 + lane];
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tm, 128);
   }
 }
 
@@ -362,13 +580,13 @@ static inline int blocks_of(int n, int size) { return (n + size - 1) / size; }
 
 extern "C" size_t hsa_block_scores_workspace_size(int M, int L, int H, int block_k) {
   if (M <= 0 || L <= 0 || H <= 0 || (block_k != 64 && block_k != 128)) return 0;
-  return align256(((size_t)blocks_of(M, kRouteTile) + blocks_of(L, block_k)) * H * 128 * sizeof(float));
+  return align256(((size_t)blocks_of(M, kRouteTile) + blocks_of(L, block_k)) * H * 128 * 3 * sizeof(__nv_bfloat16));
 }
 
 extern "C" int hsa_block_scores(const void* d_q, int M, const void* d_k, int L, int H, int dtype, int block_k,
                                 float* d_scores, void* d_ws, size_t ws_bytes, void* stream) {
   if (dtype != HSA_BF16 && dtype != HSA_F32) return set_error(HSA_EINVAL, "block_scores: unknown dtype");
-  if (M < 0 || L <= 0 || H <= 0 || H > 65535) return set_error(HSA_EINVAL, "block_scores: need M >= 0, L > 0 and H > 0");
+  if (M < 0 || L <= 0 || H <= 0 || H > 4096) return set_error(HSA_EINVAL, "block_scores: need M >= 0, L > 0 and 0 < H <= 4096");
   if (block_k != 64 && block_k != 128) return set_error(HSA_EINVAL, "block_scores: need block_k = 64 or 128");
   const int T = blocks_of(M, kRouteTile), B = blocks_of(L, block_k);
   if ((long long)T + B > 65535) return set_error(HSA_EINVAL, "block_scores: more than 65535 blocks");
@@ -378,20 +596,33 @@ extern "C" int hsa_block_scores(const void* d_q, int M, const void* d_k, int L, 
   if (ws_bytes < hsa_block_scores_workspace_size(M, L, H, block_k))
     return set_error(HSA_EWORKSPACE, "block_scores: workspace smaller than hsa_block_scores_workspace_size");
   cudaStream_t st = as_stream(stream);
-  float* means = static_cast<float*>(d_ws);
+  __nv_bfloat16* means = static_cast<__nv_bfloat16*>(d_ws);
   ScopedTiming timing(HSA_KCLASS_OTHER, st);
-  const dim3 g1((unsigned)H, (unsigned)(T + B));
-  if (dtype == HSA_BF16)
-    launch(k_block_means<__nv_bfloat16>, g1, 256, 0, st, static_cast<const __nv_bfloat16*>(d_q), M,
-           static_cast<const __nv_bfloat16*>(d_k), L, H, block_k, T, means);
-  else
-    launch(k_block_means<float>, g1, 256, 0, st, static_cast<const float*>(d_q), M, static_cast<const float*>(d_k), L,
-           H, block_k, T, means);
-  count_launch(1);
-  int rc = check_launch("block means launch");
+  static PerContextOnce attr;
+  int rc = attr.ensure([](void**) {
+    if (cudaFuncSetAttribute(k_block_product, cudaFuncAttributeMaxDynamicSharedMemorySize, kProdSmem) != cudaSuccess)
+      return check_launch("block_scores: shared-memory attribute");
+    return (int)HSA_OK;
+  });
   if (rc) return rc;
-  launch(k_block_product, dim3((unsigned)blocks_of(B, 64), (unsigned)blocks_of(T, 64), (unsigned)H), 256, 0, st, means,
-         T, B, H, d_scores);
+  rc = dtype == HSA_BF16 ? launch_means<__nv_bfloat16>(d_q, M, d_k, L, H, block_k, T, B, means, st)
+                         : launch_means<float>(d_q, M, d_k, L, H, block_k, T, B, means, st);
+  if (rc) return rc;
+  count_launch(1);
+  rc = check_launch("block means launch");
+  if (rc) return rc;
+  CUtensorMap ta, tb;
+  const uint64_t planes = 3 * (uint64_t)(T + B);
+  rc = make_tmap_2d(&ta, means, true, (uint64_t)H * 128, planes, (uint64_t)H * 256, 64, 128, true);
+  if (!rc) rc = make_tmap_2d(&tb, means, true, (uint64_t)H * 128, planes, (uint64_t)H * 256, 64, 64, true);
+  if (rc) return rc;
+  // ranges of block tiles: as many CTAs as SMs while a head's 128 query tiles leave some idle, else ranges
+  // of about six tiles (the query side is loaded once per range)
+  const int tiles_b = blocks_of(B, 64), units = blocks_of(T, 128) * H;
+  int ranges = num_sms() / units > blocks_of(tiles_b, 6) ? num_sms() / units : blocks_of(tiles_b, 6);
+  ranges = ranges > tiles_b ? tiles_b : ranges;
+  launch(k_block_product, dim3((unsigned)ranges, (unsigned)blocks_of(T, 128), (unsigned)H), 192, kProdSmem, st, ta, tb,
+         T, B, d_scores);
   count_launch(1);
   return check_launch("block product launch");
 }
