@@ -489,13 +489,13 @@ __global__ void __launch_bounds__(kSpThreads, 1)
           const float den = aF * xl[done_first][row] + aG * xl[done_first ^ 1u][row];
           const float inv_l = den > 0.f ? 1.0f / den : 0.f;
           const float wF = done_slot >= 0 ? aF : aF * inv_l, wG = done_slot >= 0 ? aG : aG * inv_l;
-          if (done_slot >= 0 && par == 0)
-            grid.part_ml[(size_t)done_slot * kAttnBM + row] = make_float2(mm, den);
+          const int m0 = (done_u % grid.QT) * kAttnBM;
+          const bool part = done_slot >= 0 && m0 + row < M;
+          if (part && par == 0) grid.part_ml[(size_t)done_slot * kAttnBM + row] = make_float2(mm, den);
           mbar_wait(&sh->o_done, pb);
           __syncwarp();
           tc_fence_after();
           // this warp writes output columns [64 par, 64 par + 64) of its 32 rows, 32 at a time
-          const int m0 = (done_u % grid.QT) * kAttnBM;
           uint4 ch[2][4];                                 // the row's 64 columns in bf16, chunks of 8
 #pragma unroll
           for (int hc = 0; hc < 2; ++hc) {
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
               const float g = done_two ? __uint_as_float(oG[e]) : 0.f;
               f[e] = fmaf(__uint_as_float(oF[e]), wF, g * wG);
             }
-            if (done_slot >= 0) {
+            if (part) {
               float* dst = grid.part_o + ((size_t)done_slot * kAttnBM + row) * 128 + col;
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
@@ -654,8 +654,38 @@ __global__ void __launch_bounds__(kSpThreads, 1)
   }
 }
 
-// Merge of the list ranges of the split units, as k_attn_combine; a range without keys has sum 0 and
-// wrote no O.  One warp per (unit, row), lane = 4 channels.
+// Row of a split unit from its S <= 32 list ranges, by one warp: lane s holds range s's max and sum, then
+// every lane 4 channels, eight ranges' loads in flight (one after the other they cost the row S trips to
+// L2).  A range without keys has sum 0 and wrote no O.  EX: exponential of the ranges' logit units.
+template <typename EX>
+__device__ __forceinline__ float4 merge_ranges(const float* __restrict__ part_o, const float2* __restrict__ part_ml,
+                                               size_t first, size_t stride, int S, int lane, EX ex) {
+  const float2 ml = lane < S ? part_ml[first + (size_t)lane * stride] : make_float2(-INFINITY, 0.f);
+  float mx = ml.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float a = ml.y > 0.f ? ex(ml.x - mx) : 0.f;
+  const float den = warp_sum(a * ml.y);
+  const float w = den > 0.f ? a / den : 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < S; s0 += 8) {
+    float4 v[8];
+    float ws[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      ws[i] = __shfl_sync(0xffffffffu, w, (s0 + i) & 31);
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s0 + i < S && ws[i] > 0.f) v[i] = ld4(part_o + (first + (size_t)(s0 + i) * stride) * 128 + lane * 4);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (s0 + i < S)
+        acc = make_float4(fmaf(ws[i], v[i].x, acc.x), fmaf(ws[i], v[i].y, acc.y), fmaf(ws[i], v[i].z, acc.z),
+                          fmaf(ws[i], v[i].w, acc.w));
+  }
+  return acc;
+}
+
 __global__ void __launch_bounds__(256) k_attn_sparse_combine(const float* __restrict__ part_o,
                                                              const float2* __restrict__ part_ml, int n_tail,
                                                              int s_tail, int u_full, int QT, int M, int H,
@@ -666,22 +696,9 @@ __global__ void __launch_bounds__(256) k_attn_sparse_combine(const float* __rest
   if (tu >= n_tail) return;
   const int u = u_full + tu, grow = (u % QT) * kAttnBM + row, h = u / QT;
   if (grow >= M) return;
-  float mx = -INFINITY;
-  for (int sp = 0; sp < s_tail; ++sp) mx = fmaxf(mx, part_ml[(size_t)(tu * s_tail + sp) * kAttnBM + row].x);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float den = 0.f;
-  for (int sp = 0; sp < s_tail; ++sp) {
-    const size_t r = (size_t)(tu * s_tail + sp) * kAttnBM + row;
-    const float2 ml = part_ml[r];
-    if (ml.y == 0.f) continue;
-    const float a = exp2f(ml.x - mx);
-    den = fmaf(a, ml.y, den);
-    const float4 o = ld4(part_o + r * 128 + lane * 4);
-    acc = make_float4(fmaf(a, o.x, acc.x), fmaf(a, o.y, acc.y), fmaf(a, o.z, acc.z), fmaf(a, o.w, acc.w));
-  }
-  const float inv = den > 0.f ? 1.0f / den : 0.f;
-  store4(O + (size_t)grow * (H * 128) + h * 128 + lane * 4,
-         make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  const float4 o = merge_ranges(part_o, part_ml, (size_t)tu * s_tail * kAttnBM + row, kAttnBM, s_tail, lane,
+                                [](float x) { return exp2f(x); });
+  store4(O + (size_t)grow * (H * 128) + h * 128 + lane * 4, o);
 }
 
 // ------------------------------------------------------------------ float32, CUDA cores
@@ -696,139 +713,176 @@ __device__ __forceinline__ void stage_rows(const SparseList& s, size_t unit, int
   }
 }
 
-// The full-context fp32 kernel's tiling (k_attn_f32: 32 query rows per CTA, 64-key tiles) over the list
-// of the rows' query tile; a 128-row block is two tiles.
-__global__ void __launch_bounds__(256, 2)
+// CTA = 64 query rows of one head x a range of their tile's list, 64 keys at a time (a 128-row block is two
+// tiles).  128 threads; thread (ty, tx) has rows 8 ty .. 8 ty + 7, logits of keys tx + 16 j (j < 4) and
+// output channels 4 tx .. and 64 + 4 tx ...  Bound by shared-memory reads, so the thread tiles are 8 x 4 and
+// 8 x 8, products run in packed pairs, and P is kept key by key so that a thread's eight weights are two reads
+// (2 x 4 and 2 x 8 tiles with P row by row, as in k_attn_f32, read three times as much: 22.7 against 16.1 us
+// for 512 rows x 8 of 16 blocks of 64, 2 heads).  Tiles come by 16-byte asynchronous copies: K of the next
+// tile travels while this one's softmax and P V run, V while the next Q K^T does.
+constexpr int kSp32BQ = 64, kSp32BK = 64, kSp32Ld = 132, kSp32PLd = 68;
+constexpr int kSp32Smem = ((kSp32BQ + 2 * kSp32BK) * kSp32Ld + kSp32BK * kSp32PLd) * 4;
+
+__device__ __forceinline__ void copy16_async(float* dst, const float* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__global__ void __launch_bounds__(128, 1)
     k_attn_sparse_f32(const float* __restrict__ Q, int M, const float* __restrict__ K, const float* __restrict__ V,
                       int L, int H, int n_split, const SparseList sl, float* __restrict__ O,
                       float* __restrict__ part_o, float2* __restrict__ part_ml) {
   pdl_prologue();
   extern __shared__ float4 sm4[];
-  float* Qs = reinterpret_cast<float*>(sm4);
-  float* Ks = Qs + kF32BQ * kF32Ld;
-  float* Vs = Ks + kF32BK * kF32Ld;
-  float* Ps = Vs + kF32BK * kF32Ld;
-  constexpr int kPsLd = kF32BK + 4;
-  int* rows = reinterpret_cast<int*>(Ps + kF32BQ * kPsLd);
+  float* Qs = reinterpret_cast<float*>(sm4);              // [64][132]
+  float* Ks = Qs + kSp32BQ * kSp32Ld;                     // [64][132]
+  float* Vs = Ks + kSp32BK * kSp32Ld;                     // [64][132]
+  float* Ps = Vs + kSp32BK * kSp32Ld;                     // [64 keys][68]
+  int* rows = reinterpret_cast<int*>(Ps + kSp32BK * kSp32PLd);
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const int QB = (M + kF32BQ - 1) / kF32BQ, QT = (M + HSA_QUERY_TILE - 1) / HSA_QUERY_TILE;
+  const int QB = (M + kSp32BQ - 1) / kSp32BQ, QT = (M + HSA_QUERY_TILE - 1) / HSA_QUERY_TILE;
   int b = blockIdx.x;
   const int split = b % n_split;
   b /= n_split;
   const int qb = b % QB, h = b / QB;
-  const int D = H * 128, m0 = qb * kF32BQ;
+  const int D = H * 128, m0 = qb * kSp32BQ;
   const size_t unit = (size_t)h * QT + m0 / HSA_QUERY_TILE;
+#pragma unroll
+  for (int i = 0; i < kSp32BQ / 4; ++i) {
+    const int r = (tid >> 5) + 4 * i, c4 = tid & 31;
+    const bool ok = m0 + r < M;
+    copy16_async(Qs + r * kSp32Ld + 4 * c4, Q + (size_t)(ok ? m0 + r : m0) * D + h * 128 + 4 * c4, ok);
+  }
   const int n_list = listed_blocks(sl, unit);
-  const int per = sl.block / kF32BK;                      // tiles per block
+  const int per = sl.block / kSp32BK;                     // tiles per block
   const int i0 = (int)((long long)split * n_list / n_split);
   const int i1 = (int)((long long)(split + 1) * n_list / n_split);
   stage_rows(sl, unit, i0, i1 - i0, L, rows);
-  for (int i = tid; i < kF32BQ * 32; i += 256) {
-    const int r = i >> 5, c4 = i & 31;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m0 + r < M) v = ld4(Q + (size_t)(m0 + r) * D + h * 128 + 4 * c4);
-    st4(Qs + r * kF32Ld + 4 * c4, v);
+  __syncthreads();
+  const int nt = (i1 - i0) * per;
+  auto tile_row = [&](int t) { return per == 1 ? rows[t] : rows[t >> 1] + (t & 1) * kSp32BK; };
+  // the 64 keys from cache row k0, zeros beyond the cache
+  auto load_tile = [&](float* dst, const float* src, int k0) {
+#pragma unroll
+    for (int i = 0; i < kSp32BK / 4; ++i) {
+      const int key = (tid >> 5) + 4 * i, c4 = tid & 31;
+      const bool ok = k0 + key < L;
+      copy16_async(dst + key * kSp32Ld + 4 * c4, src + (size_t)(ok ? k0 + key : 0) * D + h * 128 + 4 * c4, ok);
+    }
+    copy_group();
+  };
+  if (nt > 0) {
+    load_tile(Ks, K, tile_row(0));                        // with Q
+    load_tile(Vs, V, tile_row(0));
   }
   const float scale = 0.08838834764831845f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float o[2][8];
+  float m[8], l[8];
+  float2 o[8][4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 8; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) o[i][c] = 0.f;
-  const float* q0r = Qs + (2 * ty) * kF32Ld;
-  const float* q1r = q0r + kF32Ld;
-  const int nt = (i1 - i0) * per;
+    for (int c = 0; c < 4; ++c) o[i][c] = make_float2(0.f, 0.f);
+  }
+  const float* qr = Qs + (8 * ty) * kSp32Ld;
   for (int t = 0; t < nt; ++t) {
-    __syncthreads();                                      // rows staged; the previous tile's reads are done
-    const int k0 = per == 1 ? rows[t] : rows[t >> 1] + (t & 1) * kF32BK;
-    for (int i = tid; i < kF32BK * 32; i += 256) {
-      const int key = i >> 5, c4 = i & 31;
-      float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-      if (k0 + key < L) {
-        kv = ld4(K + (size_t)(k0 + key) * D + h * 128 + 4 * c4);
-        vv = ld4(V + (size_t)(k0 + key) * D + h * 128 + 4 * c4);
-      }
-      st4(Ks + key * kF32Ld + 4 * c4, kv);
-      st4(Vs + key * kF32Ld + 4 * c4, vv);
-    }
+    const int k0 = tile_row(t);
+    copy_wait<1>();                                       // K_t; V_t may still travel
     __syncthreads();
-    float s[2][4];
+    float2 s2[8][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
+      for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
+#pragma unroll 2
     for (int c = 0; c < 128; c += 4) {
-      const float4 a0 = ld4(q0r + c), a1 = ld4(q1r + c);
+      float4 kk[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 kk = ld4(Ks + (tx + 16 * j) * kF32Ld + c);
-        s[0][j] = fmaf(a0.x, kk.x, fmaf(a0.y, kk.y, fmaf(a0.z, kk.z, fmaf(a0.w, kk.w, s[0][j]))));
-        s[1][j] = fmaf(a1.x, kk.x, fmaf(a1.y, kk.y, fmaf(a1.z, kk.z, fmaf(a1.w, kk.w, s[1][j]))));
+      for (int j = 0; j < 4; ++j) kk[j] = ld4(Ks + (tx + 16 * j) * kSp32Ld + c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 a = ld4(qr + i * kSp32Ld + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          s2[i][j] = ffma2(make_float2(a.z, a.w), make_float2(kk[j].z, kk[j].w),
+                           ffma2(make_float2(a.x, a.y), make_float2(kk[j].x, kk[j].y), s2[i][j]));
       }
     }
-    float corr[2];
+    __syncthreads();                                      // K is read: the next one may come
+    if (t + 1 < nt) load_tile(Ks, K, tile_row(t + 1));
+    float p[8][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 8; ++i) {
       float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[i][j] = (k0 + tx + 16 * j < L) ? s[i][j] * scale : -INFINITY;
-        mx = fmaxf(mx, s[i][j]);
+        p[i][j] = (k0 + tx + 16 * j < L) ? (s2[i][j].x + s2[i][j].y) * scale : -INFINITY;
+        mx = fmaxf(mx, p[i][j]);
       }
 #pragma unroll
       for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
       const float m_new = fmaxf(m[i], mx);
       const float m_ref = m_new == -INFINITY ? 0.f : m_new;   // no key so far: every weight is 0
-      corr[i] = expf(m[i] - m_ref);
+      const float corr = expf(m[i] - m_ref);
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float p = expf(s[i][j] - m_ref);
-        sum += p;
-        Ps[(2 * ty + i) * kPsLd + tx + 16 * j] = p;
+        p[i][j] = expf(p[i][j] - m_ref);
+        sum += p[i][j];
       }
 #pragma unroll
       for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      l[i] = l[i] * corr[i] + sum;
+      l[i] = l[i] * corr + sum;
       m[i] = m_new;
-    }
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int c = 0; c < 8; ++c) o[i][c] *= corr[i];
-    const float* p0r = Ps + (2 * ty) * kPsLd;
-    const float* p1r = p0r + kPsLd;
-#pragma unroll 4
-    for (int key = 0; key < kF32BK; ++key) {
-      const float p0 = p0r[key], p1 = p1r[key];
-      const float4 va = ld4(Vs + key * kF32Ld + 8 * tx), vb = ld4(Vs + key * kF32Ld + 8 * tx + 4);
-      const float vv[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        o[0][c] = fmaf(p0, vv[c], o[0][c]);
-        o[1][c] = fmaf(p1, vv[c], o[1][c]);
+      for (int c = 0; c < 4; ++c) {
+        o[i][c].x *= corr;
+        o[i][c].y *= corr;
       }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = 2 * ty + i, grow = m0 + row;
-    if (grow >= M) continue;
-    if (n_split == 1) {
-      const float inv = l[i] > 0.f ? 1.0f / l[i] : 0.f;
-      float* dst = O + (size_t)grow * D + h * 128 + 8 * tx;
-      st4(dst, make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv));
-      st4(dst + 4, make_float4(o[i][4] * inv, o[i][5] * inv, o[i][6] * inv, o[i][7] * inv));
-    } else {
-      const size_t slot = (size_t)blockIdx.x * kF32BQ + row;
-      float* dst = part_o + slot * 128 + 8 * tx;
-      st4(dst, make_float4(o[i][0], o[i][1], o[i][2], o[i][3]));
-      st4(dst + 4, make_float4(o[i][4], o[i][5], o[i][6], o[i][7]));
-      if (tx == 0) part_ml[slot] = make_float2(m[i], l[i]);
+    for (int j = 0; j < 4; ++j) {
+      float* dst = Ps + (tx + 16 * j) * kSp32PLd + 8 * ty;
+      st4(dst, make_float4(p[0][j], p[1][j], p[2][j], p[3][j]));
+      st4(dst + 4, make_float4(p[4][j], p[5][j], p[6][j], p[7][j]));
     }
+    if (t + 1 < nt) copy_wait<1>();                       // V_t; K_{t+1} may still travel
+    else copy_wait<0>();
+    __syncthreads();
+#pragma unroll 2
+    for (int key = 0; key < kSp32BK; ++key) {
+      const float4 pa = ld4(Ps + key * kSp32PLd + 8 * ty), pb = ld4(Ps + key * kSp32PLd + 8 * ty + 4);
+      const float4 va = ld4(Vs + key * kSp32Ld + 4 * tx), vb = ld4(Vs + key * kSp32Ld + 64 + 4 * tx);
+      const float pw[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+      const float2 vv[4] = {make_float2(va.x, va.y), make_float2(va.z, va.w), make_float2(vb.x, vb.y),
+                            make_float2(vb.z, vb.w)};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[i][c] = ffma2(make_float2(pw[i], pw[i]), vv[c], o[i][c]);
+    }
+    if (t + 1 < nt) {
+      __syncthreads();                                    // V and P are read
+      load_tile(Vs, V, tile_row(t + 1));
+    }
+  }
+  if (nt == 0) copy_wait<0>();                            // Q
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = 8 * ty + i, grow = m0 + row;
+    if (grow >= M) continue;
+    const size_t slot = (size_t)blockIdx.x * kSp32BQ + row;
+    const bool whole = n_split == 1;
+    const float w = whole ? (l[i] > 0.f ? 1.0f / l[i] : 0.f) : 1.0f;
+    float* dst = (whole ? O + (size_t)grow * D + h * 128 : part_o + slot * 128) + 4 * tx;
+    st4(dst, make_float4(o[i][0].x * w, o[i][0].y * w, o[i][1].x * w, o[i][1].y * w));
+    st4(dst + 64, make_float4(o[i][2].x * w, o[i][2].y * w, o[i][3].x * w, o[i][3].y * w));
+    if (!whole && tx == 0) part_ml[slot] = make_float2(m[i], l[i]);
   }
 }
 
@@ -837,32 +891,43 @@ __global__ void __launch_bounds__(256) k_attn_sparse_f32_combine(const float* __
                                                                  int n_split, float* __restrict__ O) {
   pdl_prologue();
   const int w = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  const int QB = (M + kF32BQ - 1) / kF32BQ;
-  const int row = w % kF32BQ, unit = w / kF32BQ;
+  const int QB = (M + kSp32BQ - 1) / kSp32BQ;
+  const int row = w % kSp32BQ, unit = w / kSp32BQ;
   if (unit >= QB * H) return;
-  const int qb = unit % QB, h = unit / QB, grow = qb * kF32BQ + row;
+  const int qb = unit % QB, h = unit / QB, grow = qb * kSp32BQ + row;
   if (grow >= M) return;
-  float mx = -INFINITY;
-  for (int s = 0; s < n_split; ++s) mx = fmaxf(mx, part_ml[((size_t)unit * n_split + s) * kF32BQ + row].x);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float den = 0.f;
-  for (int s = 0; s < n_split; ++s) {
-    const size_t slot = ((size_t)unit * n_split + s) * kF32BQ + row;
-    const float2 ml = part_ml[slot];
-    if (ml.y == 0.f) continue;
-    const float a = expf(ml.x - mx);
-    den = fmaf(a, ml.y, den);
-    const float4 v = ld4(part_o + slot * 128 + 4 * lane);
-    acc = make_float4(fmaf(a, v.x, acc.x), fmaf(a, v.y, acc.y), fmaf(a, v.z, acc.z), fmaf(a, v.w, acc.w));
-  }
-  const float inv = den > 0.f ? 1.0f / den : 0.f;
-  st4(O + (size_t)grow * (H * 128) + h * 128 + 4 * lane,
-      make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  const float4 o = merge_ranges(part_o, part_ml, (size_t)unit * n_split * kSp32BQ + row, kSp32BQ, n_split, lane,
+                                [](float x) { return expf(x); });
+  st4(O + (size_t)grow * (H * 128) + h * 128 + 4 * lane, o);
 }
 
 // ------------------------------------------------------------------ host
 namespace {
 int sparse_tiles(int keep, int block) { return block == 64 ? (keep + 1) / 2 : keep; }
+
+// Ranges of the lists of an incomplete last wave's units.  Few units (a handful of query rows) against long
+// lists wait for memory, and the more SMs fetch the better: as many ranges as fill one wave.  Otherwise as
+// for the full-context kernel.
+TailSplit sparse_plan(int M, int H, int keep, int block) {
+  const int U = (M + kAttnBM - 1) / kAttnBM * H, tiles = sparse_tiles(keep, block), sms = num_sms();
+  if (2 * U <= sms) {
+    int S = sms / U < tiles ? sms / U : tiles;
+    if (S > 32) S = 32;
+    return S > 1 ? TailSplit{0, S, U} : TailSplit{U, 1, 0};
+  }
+  return plan_tail(U, tiles, sms);
+}
+
+// The fp32 kernel's list ranges: one 64-key tile or more each, one CTA per SM, partials within the workspace
+int sparse_f32_splits(int M, int H, int keep, int block, size_t ws_bytes) {
+  const long long units = (long long)((M + kSp32BQ - 1) / kSp32BQ) * H;
+  long long S = num_sms() / units;
+  if (S > keep) S = keep;
+  if (S > 32) S = 32;
+  const size_t per = (size_t)units * kSp32BQ * (128 * sizeof(float) + sizeof(float2));
+  if ((size_t)S * per + 256 > ws_bytes) S = ws_bytes < 256 ? 1 : (long long)((ws_bytes - 256) / per);
+  return S < 1 ? 1 : (int)S;
+}
 
 int sparse_bf16(const void* Q, int M, const void* K, const void* V, int L, int H, const SparseList& sl, void* O,
                 void* ws, size_t ws_bytes, cudaStream_t st) {
@@ -881,7 +946,7 @@ int sparse_bf16(const void* Q, int M, const void* K, const void* V, int L, int H
   });
   if (rc) return rc;
   const int QT = (M + kAttnBM - 1) / kAttnBM, U = QT * H;
-  TailSplit ts = plan_tail(U, sparse_tiles(sl.keep, sl.block), num_sms());
+  TailSplit ts = sparse_plan(M, H, sl.keep, sl.block);
   const size_t need = tail_split_bytes(ts);
   if (need == 0 || !ws || ws_bytes < need) ts = TailSplit{U, 1, 0};
   AttnGrid g{QT, ts.u_full, ts.s_tail, nullptr, nullptr};
@@ -907,25 +972,23 @@ int sparse_f32(const float* Q, int M, const float* K, const float* V, int L, int
   static PerContextOnce attr;
   int rc = attr.ensure([](void**) {
     if (cudaFuncSetAttribute(k_attn_sparse_f32, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kF32AttnSmem + 4 * HSA_SPARSE_MAX_KEEP) != cudaSuccess)
+                             kSp32Smem + 4 * HSA_SPARSE_MAX_KEEP) != cudaSuccess)
       return check_launch("sparse attention (fp32): shared-memory attribute");
     return (int)HSA_OK;
   });
   if (rc) return rc;
-  const int QB = (M + kF32BQ - 1) / kF32BQ;
-  int S = ws ? f32_attn_splits(M, sl.keep * sl.block, H, ws_bytes) : 1;
-  const size_t slots = (size_t)QB * H * S * kF32BQ;
-  const size_t o_bytes = align256(slots * 128 * sizeof(float));
-  if (S > 1 && o_bytes + slots * sizeof(float2) > ws_bytes) S = 1;
+  const int QB = (M + kSp32BQ - 1) / kSp32BQ;
+  const int S = ws ? sparse_f32_splits(M, H, sl.keep, sl.block, ws_bytes) : 1;
+  const size_t o_bytes = align256((size_t)QB * H * S * kSp32BQ * 128 * sizeof(float));
   float* part_o = S > 1 ? static_cast<float*>(ws) : nullptr;
   float2* part_ml = S > 1 ? reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + o_bytes) : nullptr;
   ScopedTiming timing(HSA_KCLASS_ATTENTION, st);
-  launch(k_attn_sparse_f32, (unsigned)(QB * H * S), 256, kF32AttnSmem + 4 * sl.keep, st, Q, M, K, V, L, H, S, sl, O,
+  launch(k_attn_sparse_f32, (unsigned)(QB * H * S), 128, kSp32Smem + 4 * sl.keep, st, Q, M, K, V, L, H, S, sl, O,
          part_o, part_ml);
   count_launch(1);
   rc = check_launch("sparse attention (fp32) launch");
   if (rc || S == 1) return rc;
-  const long long warps = (long long)QB * H * kF32BQ;
+  const long long warps = (long long)QB * H * kSp32BQ;
   launch(k_attn_sparse_f32_combine, (unsigned)((warps + 7) / 8), 256, 0, st, part_o, part_ml, M, H, S, O);
   count_launch(1);
   return check_launch("sparse attention (fp32) combine launch");
@@ -938,9 +1001,14 @@ using namespace hsa;
 
 extern "C" size_t hsa_sparse_attention_workspace_size(int M, int L, int H, int dtype, int block_k, int keep) {
   if (M <= 0 || L <= 0 || H <= 0 || keep < 1 || keep > HSA_SPARSE_MAX_KEEP || (block_k != 64 && block_k != 128)) return 0;
-  if (dtype == HSA_F32) return attention_f32_split_bytes(M, keep * block_k, H);
+  if (dtype == HSA_F32) {
+    const int S = sparse_f32_splits(M, H, keep, block_k, ~size_t(0));
+    if (S <= 1) return 0;
+    const size_t slots = (size_t)((M + kSp32BQ - 1) / kSp32BQ) * H * S * kSp32BQ;
+    return align256(slots * 128 * sizeof(float)) + align256(slots * sizeof(float2)) + 256;
+  }
   if (dtype != HSA_BF16) return 0;
-  return tail_split_bytes(plan_tail((M + kAttnBM - 1) / kAttnBM * H, sparse_tiles(keep, block_k), num_sms()));
+  return tail_split_bytes(sparse_plan(M, H, keep, block_k));
 }
 
 extern "C" int hsa_sparse_attention(const void* d_q, int M, const void* d_k, const void* d_v, int L, int H, int dtype,

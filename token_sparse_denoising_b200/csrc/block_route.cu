@@ -32,8 +32,8 @@ __device__ __forceinline__ void widen8(const uint4& u, float (&v)[8]) {
 // one or two boxes; the SMs walk the items side by side, so rows are read whole.  Warp 8 issues the loads;
 // warps 0-7 take every eighth row of a box, 16 bytes of columns a lane, and leave their sums in shared
 // memory; warps 9-10 join them and write the means while the next item is summed.  (Joined by the summing
-// warps behind a barrier, every item cost them its latency: 84 against 7x us for 40950 rows of 5120 in blocks
-// of 64; plain loads with eight in flight per warp: 42 us for 65520 rows of 1536, this 3x, a bare TMA read
+// warps behind a barrier, every item cost them its latency: 79 against 72 us for 40950 rows of 5120 in blocks
+// of 64; plain loads with eight in flight per warp: 42 us for 65520 rows of 1536, this 37, a bare TMA read
 // without sums 33.)  Rows and columns beyond the matrix arrive as zeros.  Items [0, T) x columns are the
 // query tiles, then the key blocks.  Sums in float32 (at most 128 terms).
 constexpr int kMeanSlots = 6, kMeanBox = 64 * 512, kMeanParts = 3;
