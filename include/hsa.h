@@ -376,6 +376,24 @@ int hsa_sparse_attention(const void* d_q, int M, const void* d_k, const void* d_
                          int block_k, const int32_t* d_list, int keep, const int32_t* d_count, void* d_o,
                          void* d_ws, size_t ws_bytes, void* stream);
 
+/* hsa_layer_step with block-sparse self-attention: after the cache scatter the step scores the N cached
+ * rows' blocks for each tile of 128 active rows, keeps the sp->keep best (sp->d_forced ahead of them)
+ * per tile and head, and the active rows attend to those blocks only:
+ *   hsa_block_scores(q, Kc) -> hsa_block_select(keep, d_forced) -> hsa_sparse_attention(q, Kc, Vc).
+ * The rest of the step, the arguments and the cross-attention are hsa_layer_step's.  With keep >= the
+ * number of blocks every block is listed.  N / block_k <= 16384 blocks.  Workspace:
+ * hsa_layer_step_sparse_workspace_size(M, N, D, F, dtype, sp) bytes (0: sp or a size is not allowed). */
+typedef struct hsa_block_sparsity {
+  int block_k;                  /* 64 or 128 cache rows a block                               */
+  int keep;                     /* blocks listed per tile and head, 1..HSA_SPARSE_MAX_KEEP    */
+  const uint8_t* d_forced;      /* [ceil(N / block_k)] or NULL                                */
+} hsa_block_sparsity;
+size_t hsa_layer_step_sparse_workspace_size(int M, int N, int D, int F, int dtype, const hsa_block_sparsity* sp);
+int hsa_layer_step_sparse(const hsa_layer_weights* w, void* d_kcache, void* d_vcache, int N, float* d_xA,
+                          const float* d_x_src, const int32_t* d_idx, int M, const int32_t* d_pos,
+                          const void* d_ctx_k, const void* d_ctx_v, int ctx_len, const hsa_block_sparsity* sp,
+                          void* d_ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ residual update fused with its norms
  * One pass over the rows from a block's output to the next block's input, for blocks with a norm
  * before (pre) and after (post) and modulation vectors that differ between tokens:

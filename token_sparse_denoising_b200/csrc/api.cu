@@ -221,10 +221,47 @@ extern "C" size_t hsa_layer_step_workspace_size(int M, int D, int F, int dtype) 
   return align256((size_t)M * D * e) * 3 + align256((size_t)M * 3 * D * e) + align256((size_t)M * F * e);
 }
 
-extern "C" int hsa_layer_step(const hsa_layer_weights* w, void* d_kcache, void* d_vcache, int N, float* d_xA,
-                              const float* d_x_src, const int32_t* d_idx, int M, const int32_t* d_pos,
-                              const void* d_ctx_k, const void* d_ctx_v, int ctx_len, void* d_ws, size_t ws_bytes,
-                              void* stream) {
+namespace {
+// Scratch of the block-sparse self-attention, ahead of the dense step's
+struct SparseWs {
+  void *scores_ws, *attn_ws;
+  float* scores;
+  int32_t *list, *count;
+  size_t scores_bytes, attn_bytes, total;
+};
+bool sparsity_ok(const hsa_block_sparsity* sp, int N) {
+  return sp && (sp->block_k == 64 || sp->block_k == 128) && sp->keep >= 1 && sp->keep <= HSA_SPARSE_MAX_KEEP && N > 0 &&
+         (N - 1) / sp->block_k < 16384;
+}
+SparseWs carve_sparse_ws(void* base, int M, int N, int H, int dtype, const hsa_block_sparsity& sp) {
+  const size_t T = ((size_t)M + HSA_QUERY_TILE - 1) / HSA_QUERY_TILE, B = ((size_t)N + sp.block_k - 1) / sp.block_k;
+  SparseWs w;
+  w.scores_bytes = hsa_block_scores_workspace_size(M, N, H, sp.block_k);
+  w.attn_bytes = hsa_sparse_attention_workspace_size(M, N, H, dtype, sp.block_k, sp.keep);
+  uint8_t* const p0 = static_cast<uint8_t*>(base);
+  uint8_t* p = p0;
+  w.scores_ws = p;                            p += align256(w.scores_bytes);
+  w.scores = reinterpret_cast<float*>(p);     p += align256(H * T * B * 4);
+  w.list = reinterpret_cast<int32_t*>(p);     p += align256(H * T * sp.keep * 4);
+  w.count = reinterpret_cast<int32_t*>(p);    p += align256(H * T * 4);
+  w.attn_ws = p;                              p += align256(w.attn_bytes);
+  w.total = (size_t)(p - p0);
+  return w;
+}
+}  // namespace
+
+extern "C" size_t hsa_layer_step_sparse_workspace_size(int M, int N, int D, int F, int dtype,
+                                                       const hsa_block_sparsity* sp) {
+  if (M <= 0 || N < M || D <= 0 || D % 128 || F <= 0 || (dtype != HSA_BF16 && dtype != HSA_F32) || !sparsity_ok(sp, N))
+    return 0;
+  return hsa_layer_step_workspace_size(M, D, F, dtype) + carve_sparse_ws(nullptr, M, N, D / 128, dtype, *sp).total;
+}
+
+// One block on the active rows; sp (may be null): block-sparse self-attention
+static int layer_step(const hsa_layer_weights* w, void* d_kcache, void* d_vcache, int N, float* d_xA,
+                      const float* d_x_src, const int32_t* d_idx, int M, const int32_t* d_pos, const void* d_ctx_k,
+                      const void* d_ctx_v, int ctx_len, const hsa_block_sparsity* sp, void* d_ws, size_t ws_bytes,
+                      void* stream) {
   if (!w) return set_error(HSA_EINVAL, "layer_step: null weights");
   const int D = w->D, H = w->H, F = w->F, dt = w->dtype;
   if (dt != HSA_BF16 && dt != HSA_F32) return set_error(HSA_EINVAL, "layer_step: unknown dtype");
@@ -249,6 +286,16 @@ extern "C" int hsa_layer_step(const hsa_layer_weights* w, void* d_kcache, void* 
   if (ws_bytes < hsa_layer_step_workspace_size(M, D, F, dt))
     return set_error(HSA_EWORKSPACE, "layer_step: workspace smaller than hsa_layer_step_workspace_size");
 
+  SparseWs sws = {};
+  if (sp) {
+    if (!sparsity_ok(sp, N)) return set_error(HSA_EINVAL, "layer_step: block sparsity out of range");
+    sws = carve_sparse_ws(d_ws, M, N, H, dt, *sp);
+    if (ws_bytes < hsa_layer_step_workspace_size(M, D, F, dt) + sws.total)
+      return set_error(HSA_EWORKSPACE, "layer_step: workspace smaller than hsa_layer_step_sparse_workspace_size");
+    d_ws = static_cast<uint8_t*>(d_ws) + sws.total;
+    ws_bytes -= sws.total;
+  }
+
   cudaStream_t st = as_stream(stream);
   StepWs ws = carve_step_ws(d_ws, M, D, F, dt);
   // the FFN hidden region and whatever the caller's workspace has beyond it are free until the
@@ -271,8 +318,17 @@ extern "C" int hsa_layer_step(const hsa_layer_weights* w, void* d_kcache, void* 
     HSA_TRY(launch_qk_rope(static_cast<const float*>(ws.qkv), d_idx, d_pos, M, N, D, w->g_q, w->g_k,
                            static_cast<float*>(ws.q), static_cast<float*>(d_kcache), static_cast<float*>(d_vcache),
                            st));
-  // a3: full-context attention over all N cache rows
-  HSA_TRY(attention(ws.q, M, d_kcache, d_vcache, N, H, dt, ws.att, st, spare, spare_bytes));
+  // a3: attention over all N cache rows, or over the blocks chosen for each tile of 128 active rows
+  if (sp) {
+    const int T = (M + HSA_QUERY_TILE - 1) / HSA_QUERY_TILE, B = (N + sp->block_k - 1) / sp->block_k;
+    HSA_TRY(hsa_block_scores(ws.q, M, d_kcache, N, H, dt, sp->block_k, sws.scores, sws.scores_ws, sws.scores_bytes,
+                             stream));
+    HSA_TRY(hsa_block_select(sws.scores, H * T, B, sp->keep, sp->d_forced, sws.list, sws.count, stream));
+    HSA_TRY(hsa_sparse_attention(ws.q, M, d_kcache, d_vcache, N, H, dt, sp->block_k, sws.list, sp->keep, sws.count,
+                                 ws.att, sws.attn_ws, sws.attn_bytes, stream));
+  } else {
+    HSA_TRY(attention(ws.q, M, d_kcache, d_vcache, N, H, dt, ws.att, st, spare, spare_bytes));
+  }
   // a4: gated output projection into the residual stream
   HSA_TRY(linear(ws.att, M, D, w->w_o, D, w->b_o, dt, HSA_EPI_RESID, mod + 2 * D, d_xA, st));
   if (cross) {
@@ -289,6 +345,23 @@ extern "C" int hsa_layer_step(const hsa_layer_weights* w, void* d_kcache, void* 
   else HSA_TRY(launch_ln(d_xA, nullptr, d_idx, M, N, D, mod + 4 * D, mod + 3 * D, 1, static_cast<float*>(ws.h), st));
   HSA_TRY(linear(ws.h, M, D, w->w_1, F, w->b_1, dt, HSA_EPI_GELU, nullptr, ws.hid, st));
   return linear(ws.hid, M, F, w->w_2, D, w->b_2, dt, HSA_EPI_RESID, mod + 5 * D, d_xA, st);
+}
+
+extern "C" int hsa_layer_step(const hsa_layer_weights* w, void* d_kcache, void* d_vcache, int N, float* d_xA,
+                              const float* d_x_src, const int32_t* d_idx, int M, const int32_t* d_pos,
+                              const void* d_ctx_k, const void* d_ctx_v, int ctx_len, void* d_ws, size_t ws_bytes,
+                              void* stream) {
+  return layer_step(w, d_kcache, d_vcache, N, d_xA, d_x_src, d_idx, M, d_pos, d_ctx_k, d_ctx_v, ctx_len, nullptr, d_ws,
+                    ws_bytes, stream);
+}
+
+extern "C" int hsa_layer_step_sparse(const hsa_layer_weights* w, void* d_kcache, void* d_vcache, int N, float* d_xA,
+                                     const float* d_x_src, const int32_t* d_idx, int M, const int32_t* d_pos,
+                                     const void* d_ctx_k, const void* d_ctx_v, int ctx_len,
+                                     const hsa_block_sparsity* sp, void* d_ws, size_t ws_bytes, void* stream) {
+  if (!sp) return set_error(HSA_EINVAL, "layer_step: null block sparsity");
+  return layer_step(w, d_kcache, d_vcache, N, d_xA, d_x_src, d_idx, M, d_pos, d_ctx_k, d_ctx_v, ctx_len, sp, d_ws,
+                    ws_bytes, stream);
 }
 
 // ------------------------------------------------------------------ patch model around the blocks

@@ -46,6 +46,10 @@ class IterationArgsC(C.Structure):
                 ("sel_ws_bytes", sz)]
 
 
+class BlockSparsityC(C.Structure):
+    _fields_ = [("block_k", i32), ("keep", i32), ("d_forced", vp)]
+
+
 class ResidualNormArgsC(C.Structure):
     _fields_ = [("d_X", vp), ("d_X_out", vp), ("d_y", vp), ("d_out", vp), ("dtype_y", i32), ("dtype_out", i32),
                 ("M", i32), ("D", i32), ("d_b", vp), ("post", i32), ("pre", i32), ("d_post_g", vp),
@@ -96,6 +100,9 @@ _SIGS = {
     "hsa_block_select": (i32, [vp, i32, i32, i32, vp, vp, vp, vp]),
     "hsa_sparse_attention_workspace_size": (sz, [i32, i32, i32, i32, i32, i32]),
     "hsa_sparse_attention": (i32, [vp, i32, vp, vp, i32, i32, i32, i32, vp, i32, vp, vp, vp, sz, vp]),
+    "hsa_layer_step_sparse_workspace_size": (sz, [i32, i32, i32, i32, i32, C.POINTER(BlockSparsityC)]),
+    "hsa_layer_step_sparse": (i32, [C.POINTER(LayerWeightsC), vp, vp, i32, vp, vp, vp, i32, vp, vp, vp, i32,
+                                    C.POINTER(BlockSparsityC), vp, sz, vp]),
     "hsa_residual_norm": (i32, [C.POINTER(ResidualNormArgsC), vp]),
     "hsa_iteration_host": (i32, [C.POINTER(IterationArgsC), vp, vp, C.POINTER(HostSlotC), vp, vp, vp]),
 }
@@ -296,15 +303,45 @@ def context_kv_noalloc(ctx, w_kv2, b_kv2, g_k2, k2, v2, stream=None):
                                         _ptr(k2), _ptr(v2), _stream(stream)), "hsa_context_kv_noalloc")
 
 
-def layer_step_workspace_size(M: int, D: int, F: int, dtype: int) -> int:
-    return int(lib().hsa_layer_step_workspace_size(M, D, F, dtype))
+class BlockSparsity:
+    """Block-sparse self-attention of a layer step (hsa_layer_step_sparse): per tile of 128 active rows and
+    head the `keep` best-scoring blocks of `block` cache rows; `forced` (uint8 [blocks] on the device,
+    optional: pipeline.forced_blocks) are listed ahead of all others."""
+
+    def __init__(self, keep: int, block: int = 64, forced=None):
+        import torch
+        if block not in (64, 128) or not 1 <= keep <= SPARSE_MAX_KEEP:
+            raise ValueError("block must be 64 or 128 and keep in 1..4096")
+        if forced is not None:
+            _need(forced, "forced", torch.uint8)
+        self.keep, self.block, self.forced = keep, block, forced
+        self.c = BlockSparsityC(block, keep, _ptr(forced))
+
+    def check(self, N: int):
+        if self.forced is not None and self.forced.shape != (_block_count(N, self.block),):
+            raise ValueError(f"forced must have one entry per block of {self.block} of the {N} tokens")
+
+
+def layer_step_workspace_size(M: int, D: int, F: int, dtype: int, N: int | None = None,
+                              sparsity: BlockSparsity | None = None) -> int:
+    """Scratch of a layer step on up to M rows; with `sparsity` on a cache of N rows as well."""
+    if sparsity is None:
+        return int(lib().hsa_layer_step_workspace_size(M, D, F, dtype))
+    return int(lib().hsa_layer_step_sparse_workspace_size(M, N, D, F, dtype, C.byref(sparsity.c)))
 
 
 def layer_step(w: "LayerWeights", kcache, vcache, xA, idx, pos, ws, x_src=None, ctx_k=None, ctx_v=None,
-               stream=None):
+               stream=None, sparsity: BlockSparsity | None = None):
     N = kcache.shape[0]
     M = idx.shape[0]
     L = 0 if ctx_k is None else ctx_k.shape[0]
+    if sparsity is not None:
+        sparsity.check(N)
+        _check(lib().hsa_layer_step_sparse(C.byref(w.c), _ptr(kcache), _ptr(vcache), N, _ptr(xA), _ptr(x_src),
+                                           _ptr(idx), M, _ptr(pos), _ptr(ctx_k), _ptr(ctx_v), L,
+                                           C.byref(sparsity.c), _ptr(ws), ws.numel() * ws.element_size(),
+                                           _stream(stream)), "hsa_layer_step_sparse")
+        return
     _check(lib().hsa_layer_step(C.byref(w.c), _ptr(kcache), _ptr(vcache), N, _ptr(xA), _ptr(x_src), _ptr(idx), M,
                                 _ptr(pos), _ptr(ctx_k), _ptr(ctx_v), L, _ptr(ws),
                                 ws.numel() * ws.element_size(), _stream(stream)), "hsa_layer_step")

@@ -27,10 +27,35 @@ def _to_dev(a, dtype=torch.float32, device="cuda"):
     return torch.from_numpy(np.ascontiguousarray(a, np.float32)).to(device).to(dtype)
 
 
-class SingleBlockModel:
-    """One DiT block whose output rows are the velocity (latent channels C = D)."""
+def _step_workspace(N: int, D: int, F: int, dtype: int, sparsity) -> int:
+    """Scratch for a step on any 1 <= M <= N rows."""
+    if sparsity is None:
+        return hsa.layer_step_workspace_size(N, D, F, dtype)
+    sparsity.check(N)
+    # few rows split their lists over more ranges than many do, so the size is not monotonic in M
+    sizes = (hsa.layer_step_workspace_size(M, D, F, dtype, N, sparsity) for M in _tile_steps(N))
+    return max(sizes)
 
-    def __init__(self, bw, pos, N: int, bf16: bool, ctx=None, device="cuda", cache_init=None):
+
+def _tile_steps(N: int):
+    """The row counts at which a step's scratch can grow: multiples of half a query tile, and N."""
+    return [*range(hsa.QUERY_TILE // 2, N, hsa.QUERY_TILE // 2), N]
+
+
+def forced_blocks(tokens, block: int = 64) -> torch.Tensor:
+    """Blocks that hold any token of a mask (bool [N], conditioning_frame_mask for one), as
+    hsa.BlockSparsity(forced=...) takes them: uint8 [blocks] on the current CUDA device."""
+    m = np.asarray(tokens, bool)
+    m = np.pad(m, (0, -len(m) % block)).reshape(-1, block).any(1)
+    return torch.from_numpy(m.astype(np.uint8)).cuda()
+
+
+class SingleBlockModel:
+    """One DiT block whose output rows are the velocity (latent channels C = D).
+    sparsity (hsa.BlockSparsity, optional): block-sparse self-attention over the cache."""
+
+    def __init__(self, bw, pos, N: int, bf16: bool, ctx=None, device="cuda", cache_init=None, sparsity=None):
+        self.sparsity = sparsity
         self.w = hsa.LayerWeights(bw, device, bf16)
         self.bf16 = bf16
         self.N, self.D, self.F = N, self.w.D, self.w.F
@@ -41,7 +66,7 @@ class SingleBlockModel:
             self.vc = torch.zeros((N, self.D), dtype=dt, device=device)
         else:
             self.kc, self.vc = _to_dev(cache_init[0], dt, device), _to_dev(cache_init[1], dt, device)
-        self.ws = torch.empty(hsa.layer_step_workspace_size(N, self.D, self.F, self.w.dtype), dtype=torch.uint8,
+        self.ws = torch.empty(_step_workspace(N, self.D, self.F, self.w.dtype, sparsity), dtype=torch.uint8,
                               device=device)
         self.xA = torch.empty((N, self.D), dtype=torch.float32, device=device)
         self.ctx_k = self.ctx_v = None
@@ -57,14 +82,16 @@ class SingleBlockModel:
         M = idx.shape[0]
         xA = self.xA[:M]
         hsa.layer_step(self.w, self.kc, self.vc, xA, idx, self.pos, self.ws, x_src=x, ctx_k=self.ctx_k,
-                       ctx_v=self.ctx_v)
+                       ctx_v=self.ctx_v, sparsity=self.sparsity)
         return xA
 
 
 class PatchModel:
-    """Patch-embedding C -> D, a stack of blocks with one KV cache each, output head D -> C."""
+    """Patch-embedding C -> D, a stack of blocks with one KV cache each, output head D -> C.
+    sparsity (hsa.BlockSparsity, optional): block-sparse self-attention over the caches of all blocks."""
 
-    def __init__(self, pm, pos, N: int, bf16: bool, ctx=None, device="cuda"):
+    def __init__(self, pm, pos, N: int, bf16: bool, ctx=None, device="cuda", sparsity=None):
+        self.sparsity = sparsity
         self.bf16 = bf16
         dt = torch.bfloat16 if bf16 else torch.float32
         self.dtype = hsa.HSA_BF16 if bf16 else hsa.HSA_F32
@@ -77,7 +104,7 @@ class PatchModel:
         self.F = self.blocks[0].F
         self.kc = [torch.zeros((N, self.D), dtype=dt, device=device) for _ in self.blocks]
         self.vc = [torch.zeros((N, self.D), dtype=dt, device=device) for _ in self.blocks]
-        self.ws = torch.empty(hsa.layer_step_workspace_size(N, self.D, self.F, self.dtype), dtype=torch.uint8,
+        self.ws = torch.empty(_step_workspace(N, self.D, self.F, self.dtype, sparsity), dtype=torch.uint8,
                               device=device)
         self.pws = torch.empty(hsa.patch_workspace_size(N, self.D, self.C, self.dtype), dtype=torch.uint8,
                                device=device)
@@ -99,7 +126,7 @@ class PatchModel:
         hsa.patch_embed(x, idx, self.w_in, self.b_in, X, self.pws)
         for b, w in enumerate(self.blocks):
             hsa.layer_step(w, self.kc[b], self.vc[b], X, idx, self.pos, self.ws, ctx_k=self.ctx_k[b],
-                           ctx_v=self.ctx_v[b])
+                           ctx_v=self.ctx_v[b], sparsity=self.sparsity)
         hsa.velocity_head(X, self.head_mod, self.w_out, self.b_out, vA, self.pws)
         return vA
 

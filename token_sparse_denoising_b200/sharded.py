@@ -128,9 +128,10 @@ MATRICES = ("w_qkv", "w_o", "w_1", "w_2", "w_q2", "w_kv2", "w_o2")
 
 class HeadParallelBlock:
     """One rank's part of a bf16 block: its weight slices, its heads' KV cache (N x Dl) and the
-    buffers of one step for up to M active rows."""
+    buffers of one step for up to M active rows.  sparsity (hsa.BlockSparsity, optional): block-sparse
+    self-attention; every head has its own lists, so the ranks choose without a collective."""
 
-    def __init__(self, bw, shard: HeadShard, N: int, device, cache_init=None):
+    def __init__(self, bw, shard: HeadShard, N: int, device, cache_init=None, sparsity=None):
         self.s = shard
         self.N = N
         self.device = device
@@ -159,6 +160,19 @@ class HeadParallelBlock:
         self.attn_ws = torch.empty(max(hsa.attention_workspace_size(shard.M, N, len(shard.heads), hsa.HSA_BF16), 16),
                                    dtype=torch.uint8, device=device)
         self.ctx_k = self.ctx_v = None
+        self.sparsity = sparsity
+        if sparsity is not None:
+            sparsity.check(N)
+            h, block = len(shard.heads), sparsity.block
+            tiles, blocks = -(-shard.M // hsa.QUERY_TILE), -(-N // block)
+            self.scores = torch.empty((h, tiles, blocks), dtype=torch.float32, device=device)
+            self.lists = torch.empty((h, tiles, sparsity.keep), dtype=torch.int32, device=device)
+            self.counts = torch.empty((h, tiles), dtype=torch.int32, device=device)
+            self.scores_ws = torch.empty(hsa.block_scores_workspace_size(shard.M, N, h, block), dtype=torch.uint8,
+                                         device=device)
+            self.sparse_ws = torch.empty(hsa.sparse_attention_workspace_size(shard.M, N, h, hsa.HSA_BF16, block,
+                                                                             sparsity.keep),
+                                         dtype=torch.uint8, device=device)
 
     # ---------------------------------------------------------------- once per run
     def context_kv(self, ctx):
@@ -208,8 +222,15 @@ class HeadParallelBlock:
         hsa.row_sumsq(self.qkv[:, Dl:], Dl, self.ss[:, 1:], ss_stride=2)
         yield ("all_reduce", self.ss)
         hsa.qk_norm_rope_ext(self.qkv, M, D, self.ss, w["g_q"], w["g_k"], idx, pos, self.q, self.kc, self.vc)
-        # a3: the local heads attend over all N cached rows
-        hsa.attention(self.q[:M], self.kc, self.vc, len(s.heads), self.o[:M], ws=self.attn_ws)
+        # a3: the local heads attend over all N cached rows, or over the blocks each tile of rows chooses
+        if self.sparsity is None:
+            hsa.attention(self.q[:M], self.kc, self.vc, len(s.heads), self.o[:M], ws=self.attn_ws)
+        else:
+            sp, h = self.sparsity, len(s.heads)
+            hsa.block_scores(self.q[:M], self.kc, h, sp.block, self.scores, ws=self.scores_ws)
+            hsa.block_select(self.scores, sp.keep, self.lists, self.counts, forced=sp.forced)
+            hsa.sparse_attention(self.q[:M], self.kc, self.vc, h, sp.block, self.lists, self.counts, self.o[:M],
+                                 ws=self.sparse_ws)
         # a4: partial output projection, reduced onto the row owners, gated residual
         hsa.linear(self.o, w["w_o"], None, hsa.EPI_F32, self.y_full)
         yield ("reduce_scatter", self.y_loc, self.y_full)
