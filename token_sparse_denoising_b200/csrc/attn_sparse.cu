@@ -41,7 +41,11 @@ constexpr uint32_t kSpColS = 0, kSpColO = 256, kSpCols = 512;
 constexpr uint32_t kNoBlock = 0xFFFFu;
 constexpr int kSpMaxBlocks = 65535;
 constexpr int kSpCtrlRegs = 88, kSpSoftRegs = 208;       // per thread; (88 + 2 * 208) * 128 = 168 * 384
-constexpr int kSpAheadTiles = 8;
+// The next unit is claimed when this many tiles of the current one are left (a long one; shorter ones are
+// claimed up to the ring's capacity): enough to read its list meanwhile, and late enough that an SM does
+// not sit on a whole unit while others run out (lists of 0 to 77 blocks of 64: 388 us with a unit claimed
+// ahead, 381 us so)
+constexpr int kSpAheadTiles = 6;
 
 struct SparseUnit {
   int u, nt, slot;      // unit, its tiles (0: the end of the stream), partial-result slot or -1
@@ -52,6 +56,7 @@ struct SparseShared {
   uint64_t v_empty[2];
   uint64_t s_full[2], p_full[2][2], o_done, o_free;
   uint64_t unit_full[kSpUnits], unit_empty[kSpUnits];
+  uint64_t near_end;                        // the V stream is kSpAheadTiles before the end of a long unit
   uint64_t merge[4];                        // a lane quarter's two softmax warps, at a unit's end
   uint64_t clc;
   uint4 clc_answer;
@@ -182,6 +187,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
     }
     for (int q = 0; q < 4; ++q) mbar_init(&sh->merge[q], 64);
     mbar_init(&sh->clc, 1);
+    mbar_init(&sh->near_end, 1);
     fence_mbar_init();
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
@@ -201,8 +207,8 @@ __global__ void __launch_bounds__(kSpThreads, 1)
     if (warp == 2) {
       // ---------------------------------------------------------------- scheduler
       UnitCursor at;
-      uint32_t clc_phase = 0;
-      int cta = blockIdx.x, staged = 0, last_nt = 0;
+      uint32_t clc_phase = 0, end_phase = 0;
+      int cta = blockIdx.x, staged = 0;
       bool ok = true;
       while (true) {
         int nt = 0, slot = -1, u = -1;
@@ -259,14 +265,12 @@ __global__ void __launch_bounds__(kSpThreads, 1)
           if (lane == 0) sh->unit[at.s] = SparseUnit{u, nt, slot};
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh->unit_full[at.s]);
-          // one unit ahead is enough when the one just staged is long: taking more would leave other SMs
-          // idle at the end (the unit before it is finished first)
-          const int prev = at.s == 0 ? kSpUnits - 1 : at.s - 1;
-          const uint32_t prev_phase = at.s == 0 ? at.phase ^ 1u : at.phase;
           at.advance();
           ++staged;
-          last_nt = nt;
-          if (cta >= 0 && staged >= 2 && last_nt >= kSpAheadTiles) ok = warp_wait(&sh->unit_empty[prev], prev_phase) && ok;
+          if (nt >= kSpAheadTiles) {
+            ok = warp_wait(&sh->near_end, end_phase);
+            end_phase ^= 1u;
+          }
         }
         if (cta < 0 || !ok) break;
         if (lane == 0) clc_request(&sh->clc_answer, &sh->clc);
@@ -349,6 +353,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
         if (nt == 0) break;
         for (int t = 0; ok && t < nt; ++t, ++g) {
           const uint32_t b = g & 1u;
+          if (t == nt - kSpAheadTiles && lane == 0) mbar_arrive(&sh->near_end);
           ok = warp_wait(&sh->v_empty[b], ((g >> 1) & 1u) ^ 1u);
           if (!ok) break;
           if (leader) load_tile(sV + b * kTileBytes, &tmV, &sh->p_full[b][0], vc.s, t, x0);
