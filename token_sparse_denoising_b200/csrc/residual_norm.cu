@@ -9,19 +9,22 @@
 // (written, read again) and has no post-norm.
 //
 // A row lives in the registers of W warps, 4 columns (one 16-byte access) per thread and chunk, so both
-// norms see all of it without a second read.  W = 1 up to 1536 columns (48 values a thread); wider rows
-// take 2, 4 or 8 warps, and each reduction crosses them through shared memory.  All sums are float32,
+// norms see all of it without a second read.  W = 1 up to 768 columns (24 values a thread), wider rows
+// take 2 to 16 warps, and each reduction crosses them through shared memory.  All sums are float32,
 // variances of centred values.
-// One block of 16 warps per SM walks the rows.  Each group of W warps has its own ring of row slots in
+// One block of 32 warps per SM walks the rows.  Each group of W warps has its own ring of row slots in
 // shared memory, filled by bulk copies (one elected lane, an mbarrier per slot), so the next row's X
 // and y travel while this row is reduced and written; the copies bypass L1, which keeps the
 // modulation vectors that neighbouring rows share.
+// Measured, 32760 x 1536 (bf16 in and out) / 8190 x 5120 (float32 in, bf16 out): 103 / 97 us, 5.8 / 6.0 TB/s
+// of the 6.56 a copy reaches; 16 warps of 48 values a thread 111 / 102, 8 warps 127 / 119; a warp per row
+// with plain loads and no ring 150 / 122.
 #include "common.cuh"
 
 namespace hsa {
 
-constexpr int kResNormWarpD = 1536;                // widest row of one warp
-constexpr int kResNormMaxD = 8 * kResNormWarpD;
+constexpr int kResNormWarpD = 768;                // widest row of one warp
+constexpr int kResNormMaxD = 16 * kResNormWarpD;
 
 struct ResNormArgs {
   const float* X;
@@ -46,7 +49,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-constexpr int kRnWarps = 16;        // per block, one block per SM
+constexpr int kRnWarps = 32;        // per block, one block per SM
 constexpr int kRnSlots = 4;         // most row slots a group may have
 constexpr int kRnSmem = 200 * 1024; // of row slots
 
@@ -54,7 +57,7 @@ constexpr int kRnSmem = 200 * 1024; // of row slots
 template <int W>
 __device__ __forceinline__ void group_sync(int g) {
   if constexpr (W == 1) __syncwarp();
-  else asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "r"(32 * W) : "memory");
+  else asm volatile("bar.sync %0, %1;" ::"r"(g), "r"(32 * W) : "memory");
 }
 
 // Sum over the W warps of a row; the two halves of `part` alternate, so one barrier a sum is enough
@@ -110,8 +113,9 @@ __device__ __forceinline__ float4 mul4(float4 a, float4 b) {
 }
 
 // f(z[c], v[col]) for the thread's chunks of a row vector, `kRnBatch` loads in flight at a time (a load
-// that waits for the use before it costs an L1 round trip per chunk: 221 against 111 us at 32760 x 1536)
-constexpr int kRnBatch = 4;
+// that waits for the use before it costs an L1 round trip per chunk: 221 against 111 us at 32760 x 1536,
+// 16 warps; with 32 warps three, four and six in flight take 109, 107 and 103 us)
+constexpr int kRnBatch = 6;
 template <int W, int C, typename F>
 __device__ __forceinline__ void with_vector(float4 (&z)[C], const float* v, int D, int l, F&& f) {
 #pragma unroll
@@ -248,18 +252,18 @@ static int launch_resnorm(const ResNormArgs& a, const void* y, void* out, cudaSt
   return HSA_OK;
 }
 
-// W: the fewest warps whose threads hold at most 48 values; C: chunks of 4 columns a thread
+// W: the fewest warps whose threads hold at most 24 values; C: chunks of 4 columns a thread
 template <typename TY, typename TO>
 static int dispatch_resnorm(const ResNormArgs& a, const void* y, void* out, cudaStream_t st) {
   const int D = a.D;
   if (D <= 256) return launch_resnorm<1, 2, TY, TO>(a, y, out, st);
   if (D <= 512) return launch_resnorm<1, 4, TY, TO>(a, y, out, st);
-  if (D <= 1024) return launch_resnorm<1, 8, TY, TO>(a, y, out, st);
-  if (D <= kResNormWarpD) return launch_resnorm<1, 12, TY, TO>(a, y, out, st);
-  if (D <= 2 * kResNormWarpD) return launch_resnorm<2, 12, TY, TO>(a, y, out, st);
-  if (D <= 5120) return launch_resnorm<4, 10, TY, TO>(a, y, out, st);
-  if (D <= 4 * kResNormWarpD) return launch_resnorm<4, 12, TY, TO>(a, y, out, st);
-  return launch_resnorm<8, 12, TY, TO>(a, y, out, st);
+  if (D <= kResNormWarpD) return launch_resnorm<1, 6, TY, TO>(a, y, out, st);
+  if (D <= 2 * kResNormWarpD) return launch_resnorm<2, 6, TY, TO>(a, y, out, st);
+  if (D <= 4 * kResNormWarpD) return launch_resnorm<4, 6, TY, TO>(a, y, out, st);
+  if (D <= 5120) return launch_resnorm<8, 5, TY, TO>(a, y, out, st);
+  if (D <= 8 * kResNormWarpD) return launch_resnorm<8, 6, TY, TO>(a, y, out, st);
+  return launch_resnorm<16, 6, TY, TO>(a, y, out, st);
 }
 
 }  // namespace hsa
