@@ -344,8 +344,8 @@ int hsa_linear(const void* d_x, int M, int Kin, const void* d_w, int Nout, const
  *
  * Scores: the mean logit of a query tile against a block,
  *   d_scores[h][t][b] = (mean of the tile's q rows) . (mean of the block's k rows) / sqrt(128),
- * float32 sums.  d_q: M x 128H, d_k: L x 128H in dtype; d_scores: [H][T][B] float32.
- * T + B <= 65535.  Workspace: hsa_block_scores_workspace_size(M, L, H, block_k) bytes (the means). */
+ * float32 accuracy (a mean that is not finite gives NaN).  d_q: M x 128H, d_k: L x 128H in dtype;
+ * d_scores: [H][T][B] float32.  T + B <= 65535, H <= 4096.  Workspace: hsa_block_scores_workspace_size(M, L, H, block_k) bytes (the means). */
 enum { HSA_QUERY_TILE = 128, HSA_SPARSE_MAX_KEEP = 4096 };
 size_t hsa_block_scores_workspace_size(int M, int L, int H, int block_k);
 int hsa_block_scores(const void* d_q, int M, const void* d_k, int L, int H, int dtype, int block_k,
@@ -366,11 +366,12 @@ int hsa_block_select(const float* d_scores, int rows, int n_blocks, int keep, co
 /* o = softmax(q K_S^T / sqrt(128)) V_S per head, S = the rows of the blocks listed for the query's
  * tile.  d_q: M x 128H, d_k, d_v: L x 128H, d_o: M x 128H in dtype; d_list [H][T][keep], d_count [H][T]
  * as hsa_block_select writes them.  Any order of a list is accepted; an index listed twice counts its
- * keys twice; entries behind the count are not read as blocks.  A count of 0 gives rows of 0.  A
- * listed index outside [0, B) is skipped and a count outside [0, keep] clamped, and both flag HSA_EINDEX.
+ * keys twice; entries behind the count are not read as blocks.  A count of 0 gives rows of 0.
+ * B <= 65535.  A listed index outside [0, B) is skipped and a count outside [0, keep] clamped, and both flag HSA_EINDEX.
  * With a workspace of hsa_sparse_attention_workspace_size(...) bytes the lists of the last, incomplete
  * wave of work units are split into ranges that a second kernel joins, as in hsa_attention_ws (a few
- * rows against a long list need it); a smaller or NULL workspace runs every list whole. */
+ * rows against a long list need it); a smaller or NULL workspace runs every list whole.  The size is
+ * that of this call's M and keep, and not monotonic in them. */
 size_t hsa_sparse_attention_workspace_size(int M, int L, int H, int dtype, int block_k, int keep);
 int hsa_sparse_attention(const void* d_q, int M, const void* d_k, const void* d_v, int L, int H, int dtype,
                          int block_k, const int32_t* d_list, int keep, const int32_t* d_count, void* d_o,
@@ -382,7 +383,8 @@ int hsa_sparse_attention(const void* d_q, int M, const void* d_k, const void* d_
  *   hsa_block_scores(q, Kc) -> hsa_block_select(keep, d_forced) -> hsa_sparse_attention(q, Kc, Vc).
  * The rest of the step, the arguments and the cross-attention are hsa_layer_step's.  With keep >= the
  * number of blocks every block is listed.  N / block_k <= 16384 blocks.  Workspace:
- * hsa_layer_step_sparse_workspace_size(M, N, D, F, dtype, sp) bytes (0: sp or a size is not allowed). */
+ * hsa_layer_step_sparse_workspace_size(M, N, D, F, dtype, sp) bytes (0: sp or a size is not allowed), not
+ * monotonic in M: a caller that steps on different M takes the largest of their sizes. */
 typedef struct hsa_block_sparsity {
   int block_k;                  /* 64 or 128 cache rows a block                               */
   int keep;                     /* blocks listed per tile and head, 1..HSA_SPARSE_MAX_KEEP    */

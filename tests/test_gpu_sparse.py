@@ -256,6 +256,79 @@ def test_sparse_attention_skips_and_flags_bad_lists(cuda_lib, block, dtype):
     assert cuda_lib.device_status() == 0
 
 
+@pytest.mark.parametrize("split", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sparse_attention_passes_nan_on(cuda_lib, dtype, split):
+    """NaN in a listed block reaches exactly the rows whose tile and head list it (also through the joining
+    of list ranges), everything else stays as it was."""
+    M, L, H, keep, block = 200, 1000, 2, 9, 64
+    q, k, v = qkv(65, M, L, H, dtype == "bf16")
+    lists, counts = random_lists(8, H, 2, cdiv(L, block), keep, "full")
+    lists[1, 1] = np.sort(np.setdiff1d(np.arange(cdiv(L, block)), [5])[:keep])
+    lists[0, 0, :] = np.arange(keep)                       # lists block 5
+    clean = run_attention(cuda_lib, q, k, v, H, block, lists, counts, dtype, split)
+    k[5 * block + 3, :] = np.nan
+    got = run_attention(cuda_lib, q, k, v, H, block, lists, counts, dtype, split)
+    for h in range(H):
+        for t in range(2):
+            r, c = slice(128 * t, min(128 * t + 128, M)), slice(128 * h, 128 * h + 128)
+            if 5 in lists[h, t]:
+                assert np.all(np.isnan(got[r, c]))
+            else:
+                assert np.array_equal(got[r, c], clean[r, c])
+    assert np.all(np.isnan(got[:128, :128])) and not np.any(np.isnan(got[128:, 128:]))
+
+
+@pytest.mark.parametrize("block", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sparse_attention_longest_lists(cuda_lib, block, dtype):
+    """Lists of 4096 entries, far more than there are blocks, every index many times, one of them odd."""
+    M, L, H, keep = 3, 300, 1, 4096
+    q, k, v = qkv(75, M, L, H, dtype == "bf16")
+    B = cdiv(L, block)
+    lists = np.random.default_rng(3).integers(0, B, (H, 1, keep)).astype(np.int32)
+    for n in (keep, keep - 1):
+        counts = np.full((H, 1), n, np.int32)
+        want = _by_multiplicity(q, k, v, block, lists[0, 0, :n])
+        bound = attention_bound(q, k, v, H, block, lists[:, :, :1], np.ones((H, 1), np.int32), dtype)
+        rel = 4 * keep * block * U * np.abs(want).max() + bound.max()
+        for split in (True, False):
+            got = run_attention(cuda_lib, q, k, v, H, block, lists, counts, dtype, split)
+            assert np.all(np.abs(got - want) <= rel)
+
+
+def _by_multiplicity(q, k, v, block, listed):
+    times = np.bincount(listed, minlength=cdiv(k.shape[0], block))[np.arange(k.shape[0]) // block]
+    x = q.astype(float) @ k.astype(float).T / np.sqrt(128)
+    e = np.exp(x - x.max(1, keepdims=True)) * times
+    return e @ v.astype(float) / e.sum(1, keepdims=True)
+
+
+def test_operators_return_after_a_stall_and_run_again(cuda_lib):
+    """With the library's abort flag raised every wait gives up: the calls return, and after the status has been
+    read the same calls give their results."""
+    M, L, H, keep, block = 300, 3000, 2, 12, 64
+    q, k, v = qkv(77, M, L, H, True)
+    lists, counts = random_lists(9, H, 3, cdiv(L, block), keep, "uneven")
+    bf = torch.bfloat16
+    scores = torch.empty((H, 3, cdiv(L, block)), device="cuda")
+    X, y = torch.zeros((50, 1536), device="cuda"), torch.ones((50, 1536), device="cuda")
+    want = run_attention(cuda_lib, q, k, v, H, block, lists, counts, "bf16")
+    cuda_lib.block_scores(dev(q, bf), dev(k, bf), H, block, scores)
+    want_s = host(scores).copy()
+    cuda_lib.selftest_wait_timeout()
+    run_attention(cuda_lib, q, k, v, H, block, lists, counts, "bf16")
+    cuda_lib.block_scores(dev(q, bf), dev(k, bf), H, block, scores)
+    cuda_lib.residual_norm(X, y)
+    assert cuda_lib.device_status() == cuda_lib.HSA_ETIMEOUT
+    assert np.array_equal(run_attention(cuda_lib, q, k, v, H, block, lists, counts, "bf16"), want)
+    cuda_lib.block_scores(dev(q, bf), dev(k, bf), H, block, scores)
+    assert np.array_equal(host(scores), want_s)
+    X.zero_()
+    cuda_lib.residual_norm(X, y)
+    assert torch.equal(X, y) and cuda_lib.device_status() == 0
+
+
 def test_sparse_attention_far_offsets(cuda_lib):
     """A cache of more than 2^31 elements (32 heads x 560000 rows): the last blocks of the last head."""
     H, L, M, block = 32, 560000, 40, 64

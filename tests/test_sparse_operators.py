@@ -49,7 +49,7 @@ def test_block_select_refusals(lib, change, code):
     (dict(dtype=2), "EINVAL"), (dict(M=-1), "EINVAL"), (dict(L=0), "EINVAL"), (dict(H=-3), "EINVAL"),
     (dict(block=96), "EINVAL"), (dict(keep=0), "EINVAL"), (dict(keep=4097), "EINVAL"), (dict(q=None), "EINVAL"),
     (dict(v=FAKE + 4), "EINVAL"), (dict(o=None), "EINVAL"), (dict(lists=None), "EINVAL"), (dict(counts=None), "EINVAL"),
-    (dict(ws=FAKE + 8), "EINVAL"), (dict(M=0, q=None), "OK")])
+    (dict(ws=FAKE + 8), "EINVAL"), (dict(L=64 * 65535 + 1), "EINVAL"), (dict(M=0, q=None), "OK")])
 @pytest.mark.parametrize("dtype", [hsa.HSA_BF16, hsa.HSA_F32])
 def test_sparse_attention_refusals(lib, change, code, dtype):
     a = dict(q=FAKE, M=300, k=FAKE, v=FAKE, L=1000, H=2, dtype=dtype, block=64, lists=FAKE, keep=4, counts=FAKE, o=FAKE,

@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
         __syncwarp();
         if (lane == 0) fence_proxy_async_smem();          // read before the next answer is written
       }
+      if (!ok) stall_drain();
     } else if (warp == 0) {
       // ---------------------------------------------------------------- TMA producer
       const bool leader = elect_one();
@@ -367,6 +368,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
         __syncwarp();
         vc.advance();
       }
+      if (!ok) stall_drain();
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA issuer
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
@@ -455,6 +457,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
         __syncwarp();
         pc.advance();
       }
+      if (!ok) stall_drain();
     }
   } else {
     // ---------------------------------------------------------------- softmax warps
@@ -473,7 +476,10 @@ __global__ void __launch_bounds__(kSpThreads, 1)
     int done_u = -1, done_slot = -1;
     bool done_two = false;
     uint32_t done_first = 0, done_last = 0;               // parities of its first and last tile
-    while (warp_wait(&sh->unit_full[at.s], at.phase)) {
+    bool ok = true;
+    while (ok) {
+      ok = warp_wait(&sh->unit_full[at.s], at.phase);
+      if (!ok) break;
       const int nt = sh->unit[at.s].nt;                   // 0: the end
       const uint16_t* blk = lists + at.s * stride;
       float m = -INFINITY, l = 0.f;
@@ -486,7 +492,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
           const uint32_t pb = (n_unit & 1u) ^ 1u;
           const float(*xm)[128] = sh->xm[pb];
           const float(*xl)[128] = sh->xl[pb];
-          mbar_wait(&sh->merge[quarter], pb);
+          ok = mbar_wait(&sh->merge[quarter], pb) && ok;
           const float mF = xm[done_first][row], mG = xm[done_first ^ 1u][row];
           const float mm = fmaxf(mF, mG);
           const float ms = mm == -INFINITY ? 0.f : mm;    // no key at all: weights 0
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
           const int m0 = (done_u % grid.QT) * kAttnBM;
           const bool part = done_slot >= 0 && m0 + row < M;
           if (part && par == 0) grid.part_ml[(size_t)done_slot * kAttnBM + row] = make_float2(mm, den);
-          mbar_wait(&sh->o_done, pb);
+          ok = mbar_wait(&sh->o_done, pb) && ok;
           __syncwarp();
           tc_fence_after();
           // this warp writes output columns [64 par, 64 par + 64) of its 32 rows, 32 at a time
@@ -556,7 +562,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
           v1 = b1 == kNoBlock ? 0 : L - (int)b1 * sl.block;
           if (!halves) v1 -= 64;
         }
-        mbar_wait(&sh->s_full[par], s_phase);
+        ok = mbar_wait(&sh->s_full[par], s_phase) && ok;
         s_phase ^= 1u;
         __syncwarp();
         tc_fence_after();
@@ -647,7 +653,9 @@ __global__ void __launch_bounds__(kSpThreads, 1)
       first ^= (uint32_t)nt & 1u;
       ++n_unit;
       at.advance();
+      ok = __all_sync(0xffffffffu, ok);
     }
+    if (!ok) stall_drain();
   }
 
   tc_fence_before();
@@ -669,9 +677,9 @@ __device__ __forceinline__ float4 merge_ranges(const float* __restrict__ part_o,
   float mx = ml.x;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const float a = ml.y > 0.f ? ex(ml.x - mx) : 0.f;
+  const float a = ml.y != 0.f ? ex(ml.x - mx) : 0.f;      // a sum that is NaN stays one
   const float den = warp_sum(a * ml.y);
-  const float w = den > 0.f ? a / den : 0.f;
+  const float w = den != 0.f ? a / den : 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = 0; s0 < S; s0 += 8) {
     float4 v[8];
@@ -680,7 +688,7 @@ __device__ __forceinline__ float4 merge_ranges(const float* __restrict__ part_o,
     for (int i = 0; i < 8; ++i) {
       ws[i] = __shfl_sync(0xffffffffu, w, (s0 + i) & 31);
       v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (s0 + i < S && ws[i] > 0.f) v[i] = ld4(part_o + (first + (size_t)(s0 + i) * stride) * 128 + lane * 4);
+      if (s0 + i < S && ws[i] != 0.f) v[i] = ld4(part_o + (first + (size_t)(s0 + i) * stride) * 128 + lane * 4);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)

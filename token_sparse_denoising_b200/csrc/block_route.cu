@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(kMeanThreads, 1)
   __syncthreads();
   int s = 0, ps = 0;
   uint32_t phase = 0, pphase = 0;
+  bool good = true;
   for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
     const int j = item / cols, x = (item - j * cols) * 32 * V;
     const bool key = j >= n_tiles;
@@ -80,6 +81,7 @@ __global__ void __launch_bounds__(kMeanThreads, 1)
     if (warp == 8) {
       for (int b = 0; b < boxes; ++b) {
         const bool ok = __shfl_sync(0xffffffffu, mbar_wait(&sh->empty[s], phase ^ 1u), 0);
+        good = good && ok;
         __syncwarp();
         if (ok && lane == 0) {
           mbar_expect_tx(&sh->full[s], kMeanBox);
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(kMeanThreads, 1)
     } else if (warp < 8) {
       float sum[V] = {};
       for (int b = 0; b < boxes; ++b) {
-        mbar_wait(&sh->full[s], phase);
+        good = mbar_wait(&sh->full[s], phase) && good;
         __syncwarp();
         const uint8_t* box = ring + s * kMeanBox + warp * 512 + lane * 16;
         uint4 raw[8];
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(kMeanThreads, 1)
           phase ^= 1u;
         }
       }
-      mbar_wait(&sh->part_empty[ps], pphase ^ 1u);
+      good = mbar_wait(&sh->part_empty[ps], pphase ^ 1u) && good;
       __syncwarp();
 #pragma unroll
       for (int e = 0; e < V; e += 4)
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(kMeanThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->part_full[ps]);
     } else {
-      mbar_wait(&sh->part_full[ps], pphase);
+      good = mbar_wait(&sh->part_full[ps], pphase) && good;
       __syncwarp();
       const int c = ((warp - 9) * 32 + lane) * 4;
       if (c < 32 * V) {
@@ -162,6 +164,7 @@ __global__ void __launch_bounds__(kMeanThreads, 1)
       pphase ^= 1u;
     }
   }
+  if (!good) stall_drain();
 }
 
 template <typename T>
@@ -232,6 +235,7 @@ __global__ void __launch_bounds__(192, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tmem;
+  bool good = true;
   if (warp == 0) {
     const bool leader = elect_one();
     const int rows = n_tiles + n_blocks, x = h * 128;
@@ -245,6 +249,7 @@ __global__ void __launch_bounds__(192, 1)
     for (int i = 0; i < nj; ++i) {
       const int b = i & 1;
       const bool ok = __shfl_sync(0xffffffffu, mbar_wait(&b_empty[b], ((i >> 1) & 1) ^ 1), 0);
+      good = good && ok;
       __syncwarp();
       if (ok && leader) {
         mbar_expect_tx(&b_full[b], kProdB);
@@ -284,6 +289,7 @@ __global__ void __launch_bounds__(192, 1)
       }
       __syncwarp();
     }
+    good = ok;
   } else {
     // thread = row of the tile; rows staged 65 floats apart, free of bank conflicts in both directions
     const int quarter = warp & 3;
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(192, 1)
     const int rows = min(32, n_tiles - t0 - quarter * 32);
     for (int i = 0; i < nj; ++i) {
       const int b = i & 1, b0 = (j0 + i) * 64;
-      mbar_wait(&d_full[b], (i >> 1) & 1);
+      good = mbar_wait(&d_full[b], (i >> 1) & 1) && good;
       __syncwarp();
       tc_fence_after();
       uint32_t v[64];
@@ -314,6 +320,7 @@ __global__ void __launch_bounds__(192, 1)
       __syncwarp();
     }
   }
+  if (!good) stall_drain();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

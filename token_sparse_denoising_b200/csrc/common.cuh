@@ -92,6 +92,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// For a thread whose wait gave up, before it leaves its role: time for the copies and MMAs still in
+// flight to land, so that the CTA does not give up shared memory or TMEM that they write (they take
+// microseconds; 0.1 ms is far more).
+__device__ __forceinline__ void stall_drain() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 100000ull) {
+  }
+}
+
 // ------------------------------------------------------------------ clusters: rank, distributed shared memory, barrier
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;

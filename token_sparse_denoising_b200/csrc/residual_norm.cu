@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(32 * kRnWarps, 1) k_residual_norm(const ResNor
     }
   int turn = 0, s = 0;
   uint32_t phase = 0;
+  bool filled = true;
   const float one = a.modulate ? 1.0f : 0.0f;
   for (int64_t r = first; r < M; r += step) {
     // modulation row of this token; `good` is the same for the whole group
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(32 * kRnWarps, 1) k_residual_norm(const ResNor
     }
     const float* xs = reinterpret_cast<const float*>(ring + s * slot_bytes);
     const TY* ys = reinterpret_cast<const TY*>(xs + D);
-    mbar_wait(&full[g][s], phase);                        // gives up only once the library has stalled
+    filled = mbar_wait(&full[g][s], phase) && filled;     // gives up only once the library has stalled
     __syncwarp();
     const size_t base = (size_t)r * D;
     float4 z[C];
@@ -230,6 +231,7 @@ __global__ void __launch_bounds__(32 * kRnWarps, 1) k_residual_norm(const ResNor
       if (col < D) store4(out + base + col, z[c]);        // one rounding, of the finished value
     }
   }
+  if (!filled) stall_drain();
 }
 
 template <int W, int C, typename TY, typename TO>

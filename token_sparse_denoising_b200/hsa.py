@@ -459,6 +459,8 @@ def block_scores(q, k, H: int, block: int, scores, ws=None, stream=None):
     st = _current(dev, stream)
     if ws is None:
         ws = torch.empty(block_scores_workspace_size(M, L, H, block), dtype=torch.uint8, device=q.device)
+    elif ws.get_device() != dev:
+        raise ValueError("ws must be on the operands' device")
     _check(lib().hsa_block_scores(q.data_ptr(), M, k.data_ptr(), L, H, code, block, scores.data_ptr(), ws.data_ptr(),
                                   ws.numel() * ws.element_size(), st), "hsa_block_scores")
 
@@ -497,6 +499,8 @@ def sparse_attention(q, k, v, H: int, block: int, lists, counts, o, stream=None,
     if _bad(o, (M, D), dt, dev): _refuse(o, "o", (M, D), dt, dev)
     if _bad(lists, (H, T, keep), i32t, dev): _refuse(lists, "lists", (H, T, keep), i32t, dev)
     if _bad(counts, (H, T), i32t, dev): _refuse(counts, "counts", (H, T), i32t, dev)
+    if ws is not None and ws.get_device() != dev:
+        raise ValueError("ws must be on the operands' device")
     st = _current(dev, stream)
     _check(lib().hsa_sparse_attention(q.data_ptr(), M, k.data_ptr(), v.data_ptr(), L, H, code, block,
                                       lists.data_ptr(), keep, counts.data_ptr(), o.data_ptr(), _ptr(ws),
@@ -517,31 +521,36 @@ def residual_norm(X, y, X_out=None, out=None, b=None, post="none", post_g=None, 
     gate, mul, add: [D], or (n_mod, D) views of one modulation table (equal row strides) whose row is
     mod_row[token], token = idx[r] (idx None: r)."""
     import torch
-    M, D = X.shape
-    f32t, dev = torch.float32, X.get_device()
+    shape, f32t, dev = X.shape, torch.float32, X.get_device()
+    M, D = shape
     if post not in _NORMS or pre not in _NORMS:
         raise ValueError("post and pre must be 'none', 'rms' or 'layer'")
     X_out = X if X_out is None else X_out
     y_code, out_code = _dtype_code(y), HSA_F32 if out is None else _dtype_code(out)
-    if _bad(X, (M, D), f32t, dev): _refuse(X, "X", (M, D), f32t, dev)
-    if _bad(X_out, (M, D), f32t, dev): _refuse(X_out, "X_out", (M, D), f32t, dev)
-    if _bad(y, (M, D), y.dtype, dev): _refuse(y, "y", (M, D), y.dtype, dev)
-    if out is not None and _bad(out, (M, D), out.dtype, dev): _refuse(out, "out", (M, D), out.dtype, dev)
+    if X.dtype is not f32t or not X.is_contiguous(): _refuse(X, "X", shape, f32t, dev)
+    if X_out is not X and _bad(X_out, shape, f32t, dev): _refuse(X_out, "X_out", shape, f32t, dev)
+    if y.shape != shape or not y.is_contiguous() or y.get_device() != dev: _refuse(y, "y", shape, y.dtype, dev)
+    if out is not None and (out.shape != shape or not out.is_contiguous() or out.get_device() != dev):
+        _refuse(out, "out", shape, out.dtype, dev)
     if b is not None and _bad(b, (D,), f32t, dev): _refuse(b, "b", (D,), f32t, dev)
     if post_g is not None and _bad(post_g, (D,), f32t, dev): _refuse(post_g, "post_g", (D,), f32t, dev)
     if post_b is not None and _bad(post_b, (D,), f32t, dev): _refuse(post_b, "post_b", (D,), f32t, dev)
-    n_mod = step = None
+    n_mod = step = first = None
     for t in (gate, mul, add):
         if t is None:
             continue
-        shape = t.shape
-        rows = 1 if len(shape) == 1 else shape[0]
-        row_step = D if rows == 1 else t.stride(0)
-        if shape[-1] != D or len(shape) > 2 or t.stride(-1) != 1 or t.dtype is not f32t or t.get_device() != dev:
+        if first is not None and t.shape == first.shape and t.stride() == strides and t.dtype is f32t and \
+                t.get_device() == dev:
+            continue                                      # laid out like the one already looked at
+        rows = 1 if t.dim() == 1 else t.shape[0]
+        strides = t.stride()
+        if t.dim() not in (1, 2) or t.shape[-1] != D or strides[-1] != 1 or t.dtype is not f32t or \
+                t.get_device() != dev:
             raise ValueError(f"gate, mul and add must be float32 rows of {D} on X's device")
-        if n_mod is not None and (rows != n_mod or row_step != step):
+        row_step = D if rows == 1 else strides[0]
+        if first is not None and (rows != n_mod or row_step != step):
             raise ValueError("gate, mul and add must have the same rows and row stride")
-        n_mod, step = rows, row_step
+        first, n_mod, step = t, rows, row_step
     N = 0
     if mod_row is not None:
         N = mod_row.shape[0]
@@ -552,9 +561,10 @@ def residual_norm(X, y, X_out=None, out=None, b=None, post="none", post_g=None, 
         raise ValueError("several modulation rows need mod_row")
     if idx is not None and _bad(idx, (M,), torch.int32, dev): _refuse(idx, "idx", (M,), torch.int32, dev)
     st = _current(dev, stream)
-    a = ResidualNormArgsC(X.data_ptr(), X_out.data_ptr(), y.data_ptr(), _ptr(out), y_code, out_code, M, D, _ptr(b),
-                          _NORMS[post], _NORMS[pre], _ptr(post_g), _ptr(post_b), _ptr(gate), _ptr(mul), _ptr(add),
-                          1 if modulate else 0, res_scale, _ptr(mod_row), _ptr(idx), N, n_mod or 1, step or D)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    a = ResidualNormArgsC(X.data_ptr(), X_out.data_ptr(), y.data_ptr(), ptr(out), y_code, out_code, M, D, ptr(b),
+                          _NORMS[post], _NORMS[pre], ptr(post_g), ptr(post_b), ptr(gate), ptr(mul), ptr(add),
+                          1 if modulate else 0, res_scale, ptr(mod_row), ptr(idx), N, n_mod or 1, step or D)
     _check(lib().hsa_residual_norm(C.byref(a), st), "hsa_residual_norm")
 
 
