@@ -90,6 +90,10 @@ def test_residual_norm_struct_matches_the_c_compiler(tmp_path):
     import subprocess
     fields = _struct_fields("hsa_residual_norm_args")
     assert fields == [f[0] for f in hsa.ResidualNormArgsC._fields_]
+    packed = hsa.ResidualNormArgsC.PACKED
+    values = [(i + 1) * 8 for i in range(len(fields))]
+    a = hsa.ResidualNormArgsC.from_buffer_copy(packed.pack(*values))
+    assert packed.size == C.sizeof(a) and [getattr(a, f) for f in fields] == values
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None:
         pytest.skip("no C compiler")

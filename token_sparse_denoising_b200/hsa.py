@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import numpy as np
 
@@ -56,6 +57,7 @@ class ResidualNormArgsC(C.Structure):
                 ("d_post_b", vp), ("d_gate", vp), ("d_mul", vp), ("d_add", vp), ("modulate", i32),
                 ("res_scale", f32), ("d_mod_row", vp), ("d_idx", vp), ("N", i32), ("n_mod", i32),
                 ("mod_stride", C.c_int64)]
+    PACKED = struct.Struct("@PPPPiiiiPiiPPPPPifPPiiq")     # the same layout, filled in one step
 
 
 class HostSlotC(C.Structure):
@@ -103,7 +105,7 @@ _SIGS = {
     "hsa_layer_step_sparse_workspace_size": (sz, [i32, i32, i32, i32, i32, C.POINTER(BlockSparsityC)]),
     "hsa_layer_step_sparse": (i32, [C.POINTER(LayerWeightsC), vp, vp, i32, vp, vp, vp, i32, vp, vp, vp, i32,
                                     C.POINTER(BlockSparsityC), vp, sz, vp]),
-    "hsa_residual_norm": (i32, [C.POINTER(ResidualNormArgsC), vp]),
+    "hsa_residual_norm": (i32, [vp, vp]),
     "hsa_iteration_host": (i32, [C.POINTER(IterationArgsC), vp, vp, C.POINTER(HostSlotC), vp, vp, vp]),
 }
 
@@ -561,11 +563,13 @@ def residual_norm(X, y, X_out=None, out=None, b=None, post="none", post_g=None, 
         raise ValueError("several modulation rows need mod_row")
     if idx is not None and _bad(idx, (M,), torch.int32, dev): _refuse(idx, "idx", (M,), torch.int32, dev)
     st = _current(dev, stream)
-    ptr = lambda t: None if t is None else t.data_ptr()
-    a = ResidualNormArgsC(X.data_ptr(), X_out.data_ptr(), y.data_ptr(), ptr(out), y_code, out_code, M, D, ptr(b),
-                          _NORMS[post], _NORMS[pre], ptr(post_g), ptr(post_b), ptr(gate), ptr(mul), ptr(add),
-                          1 if modulate else 0, res_scale, ptr(mod_row), ptr(idx), N, n_mod or 1, step or D)
-    _check(lib().hsa_residual_norm(C.byref(a), st), "hsa_residual_norm")
+    a = ResidualNormArgsC.PACKED.pack(
+        X.data_ptr(), X_out.data_ptr(), y.data_ptr(), 0 if out is None else out.data_ptr(), y_code, out_code, M, D,
+        0 if b is None else b.data_ptr(), _NORMS[post], _NORMS[pre], 0 if post_g is None else post_g.data_ptr(),
+        0 if post_b is None else post_b.data_ptr(), 0 if gate is None else gate.data_ptr(),
+        0 if mul is None else mul.data_ptr(), 0 if add is None else add.data_ptr(), 1 if modulate else 0, res_scale,
+        0 if mod_row is None else mod_row.data_ptr(), 0 if idx is None else idx.data_ptr(), N, n_mod or 1, step or D)
+    _check(lib().hsa_residual_norm(a, st), "hsa_residual_norm")
 
 
 class HostSlot:
