@@ -85,7 +85,8 @@ def score_rows(seed, rows, B, kind):
 
 @pytest.mark.parametrize("rows,B,keep", [(1, 1, 1), (3, 1, 5), (9, 31, 4), (7, 128, 128), (8, 129, 17), (5, 256, 255),
                                          (20, 500, 33), (17, 1182, 177), (4, 1281, 1280), (3, 2048, 1), (3, 2049, 300),
-                                         (2, 4097, 4096), (2, 16384, 1000), (1, 100, 4096)])
+                                         (2, 4097, 4096), (2, 16384, 1000), (1, 100, 4096), (7, 300, 40),
+                                         (5, 700, 90), (6, 1000, 150), (3, 2700, 400), (2, 4000, 600)])
 @pytest.mark.parametrize("kind", ["rand", "ties", "const", "closed"])
 @pytest.mark.parametrize("forced", [None, "some", "all"])
 def test_block_select_bit_exact(cuda_lib, rows, B, keep, kind, forced):

@@ -349,7 +349,7 @@ __device__ __forceinline__ float route_value(uint32_t k) {
 
 constexpr int kRouteFew = 32;      // keys a warp ranks against each other to finish the search
 
-// One row of scores per group of W warps (W = 1: 8 rows a block; W = 8: one).  Warp w of the group
+// One row of scores per group of W warps (W = 1: 8 rows a block; else the block is one group).  Warp w of the group
 // holds blocks [w 32 V, (w + 1) 32 V) in registers, 32 consecutive ones at a time.
 // The cut is searched between keys lo and hi with count(key >= lo) > keep > count(key >= hi): a pass counts
 // the keys at or above a candidate and replaces one bound, and the search ends when the count is `keep`
@@ -361,11 +361,11 @@ constexpr int kRouteFew = 32;      // keys a warp ranks against each other to fi
 // Then the chosen blocks are written in index order.  Bound by instructions: a row of 1182 scores
 // takes a warp about 1500, against 4.7 KB read.
 template <int W, int V>
-__global__ void __launch_bounds__(256, V > 40 ? 1 : V > 16 ? 3 : 4)
+__global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, W == 1 ? (V > 16 ? 3 : 4) : (V > 40 ? 8 : 24) / W)
     k_block_select(const float* __restrict__ scores, int rows, int n_blocks, int keep,
                    const uint8_t* __restrict__ forced, int* __restrict__ list, int* __restrict__ count) {
   pdl_prologue();
-  __shared__ uint32_t part[2][3][8];
+  __shared__ uint32_t part[2][3][W];
   __shared__ uint32_t fbits[W * V];
   __shared__ __align__(16) uint32_t few[W == 1 && V > 8 ? 8 : 1][kRouteFew];
   int turn = 0;
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(256, V > 40 ? 1 : V > 16 ? 3 : 4)
   const int row = W == 1 ? (int)blockIdx.x * 8 + warp : (int)blockIdx.x;
   if (forced) {
     // one bit per block, read by every row of the CTA
-    for (int i = warp; i < W * V; i += 8) {
+    for (int i = warp; i < W * V; i += (W == 1 ? 8 : W)) {
       const int b = 32 * i + lane;
       const uint32_t m = __ballot_sync(0xffffffffu, b < n_blocks && forced[b] != 0);
       if (lane == 0) fbits[i] = m;
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(256, V > 40 ? 1 : V > 16 ? 3 : 4)
   hi = __reduce_max_sync(0xffffffffu, hi);
   lo = __reduce_min_sync(0xffffffffu, lo);
   if constexpr (W > 1) {
-    uint32_t(*p)[8] = part[turn & 1];
+    uint32_t(*p)[W] = part[turn & 1];
     ++turn;
     if (lane == 0) {
       p[1][warp] = hi;
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(256, V > 40 ? 1 : V > 16 ? 3 : 4)
     }
     n_above = __reduce_add_sync(0xffffffffu, n_above);
     n_tie = __reduce_add_sync(0xffffffffu, n_tie);
-    uint32_t(*p)[8] = part[turn & 1];
+    uint32_t(*p)[W] = part[turn & 1];
     if (lane == 0) {
       p[1][warp] = n_above;
       p[2][warp] = n_tie;
@@ -575,8 +575,8 @@ __global__ void __launch_bounds__(256, V > 40 ? 1 : V > 16 ? 3 : 4)
 template <int W, int V>
 static void launch_select(const float* s, int rows, int n_blocks, int keep, const uint8_t* f, int* list, int* count,
                           cudaStream_t st) {
-  launch(k_block_select<W, V>, W == 1 ? (unsigned)(rows + 7) / 8 : (unsigned)rows, 256, 0, st, s, rows, n_blocks, keep,
-         f, list, count);
+  launch(k_block_select<W, V>, W == 1 ? (unsigned)(rows + 7) / 8 : (unsigned)rows, W == 1 ? 256 : 32 * W, 0, st, s, rows,
+         n_blocks, keep, f, list, count);
 }
 
 }  // namespace hsa
@@ -643,13 +643,23 @@ extern "C" int hsa_block_select(const float* d_scores, int rows, int n_blocks, i
   if (!d_scores || !d_list || !d_count) return set_error(HSA_EINVAL, "block_select: null pointer");
   cudaStream_t st = as_stream(stream);
   ScopedTiming timing(HSA_KCLASS_OTHER, st);
+  // the fewest warps that hold a row with at most 40 keys a lane (64 keys a lane leave an SM too few warps: 24
+  // million scores in rows of 1500 122 us, with two warps of 24 79), then the next size of the register array
   const int v = blocks_of(n_blocks, 32);
-  if (v <= 4) launch_select<1, 4>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
+  if (v <= 2) launch_select<1, 2>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
+  else if (v <= 4) launch_select<1, 4>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
   else if (v <= 8) launch_select<1, 8>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
+  else if (v <= 12) launch_select<1, 12>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
   else if (v <= 16) launch_select<1, 16>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
+  else if (v <= 24) launch_select<1, 24>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
+  else if (v <= 32) launch_select<1, 32>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
   else if (v <= 40) launch_select<1, 40>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
-  else if (v <= 64) launch_select<1, 64>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
-  else if (v <= 128) launch_select<8, 16>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
+  else if (v <= 2 * 24) launch_select<2, 24>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
+  else if (v <= 2 * 32) launch_select<2, 32>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
+  else if (v <= 2 * 40) launch_select<2, 40>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
+  else if (v <= 4 * 24) launch_select<4, 24>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
+  else if (v <= 4 * 32) launch_select<4, 32>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
+  else if (v <= 8 * 32) launch_select<8, 32>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
   else launch_select<8, 64>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
   count_launch(1);
   return check_launch("block_select launch");
