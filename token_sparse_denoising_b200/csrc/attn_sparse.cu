@@ -726,15 +726,18 @@ __device__ __forceinline__ void stage_rows(const SparseList& s, size_t unit, int
   }
 }
 
-// CTA = 64 query rows of one head x a range of their tile's list, 64 keys at a time (a 128-row block is two
-// tiles).  128 threads; thread (ty, tx) has rows 8 ty .. 8 ty + 7, logits of keys tx + 16 j (j < 4) and
+// CTA = BQ query rows of one head x a range of their tile's list, 64 keys at a time (a 128-row block is two
+// tiles).  2 BQ threads; thread (ty, tx) has rows 8 ty .. 8 ty + 7, logits of keys tx + 16 j (j < 4) and
 // output channels 4 tx .. and 64 + 4 tx ...  Bound by shared-memory reads, so the thread tiles are 8 x 4 and
 // 8 x 8, products run in packed pairs, and P is kept key by key so that a thread's eight weights are two reads
 // (2 x 4 and 2 x 8 tiles with P row by row, as in k_attn_f32, read three times as much: 22.7 against 16.1 us
 // for 512 rows x 8 of 16 blocks of 64, 2 heads).  Tiles come by 16-byte asynchronous copies: K of the next
-// tile travels while this one's softmax and P V run, V while the next Q K^T does.
-constexpr int kSp32BQ = 64, kSp32BK = 64, kSp32Ld = 132, kSp32PLd = 68;
-constexpr int kSp32Smem = ((kSp32BQ + 2 * kSp32BK) * kSp32Ld + kSp32BK * kSp32PLd) * 4;
+// tile travels while this one's softmax and P V run, V while the next Q K^T does.  BQ = 128 gives an SM eight
+// warps to hide the reads' latency with (2000 x 16 of 63 blocks of 64, 8 heads: 264 us, with 64 rows 308);
+// BQ = 64 makes twice the CTAs, for calls that would leave SMs idle.
+constexpr int kSp32BK = 64, kSp32Ld = 132;
+constexpr int sparse_f32_smem(int bq) { return ((bq + 2 * kSp32BK) * kSp32Ld + kSp32BK * (bq + 4)) * 4; }
+static_assert(sparse_f32_smem(128) + 4 * HSA_SPARSE_MAX_KEEP <= 227 * 1024, "the longest list must fit shared memory");
 
 __device__ __forceinline__ void copy16_async(float* dst, const float* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
@@ -745,28 +748,30 @@ __device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_gro
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-__global__ void __launch_bounds__(128, 1)
+template <int BQ>
+__global__ void __launch_bounds__(2 * BQ, 1)
     k_attn_sparse_f32(const float* __restrict__ Q, int M, const float* __restrict__ K, const float* __restrict__ V,
                       int L, int H, int n_split, const SparseList sl, float* __restrict__ O,
                       float* __restrict__ part_o, float2* __restrict__ part_ml) {
   pdl_prologue();
+  constexpr int kWarps = BQ / 16;
   extern __shared__ float4 sm4[];
-  float* Qs = reinterpret_cast<float*>(sm4);              // [64][132]
-  float* Ks = Qs + kSp32BQ * kSp32Ld;                     // [64][132]
+  float* Qs = reinterpret_cast<float*>(sm4);              // [BQ][132]
+  float* Ks = Qs + BQ * kSp32Ld;                     // [64][132]
   float* Vs = Ks + kSp32BK * kSp32Ld;                     // [64][132]
-  float* Ps = Vs + kSp32BK * kSp32Ld;                     // [64 keys][68]
-  int* rows = reinterpret_cast<int*>(Ps + kSp32BK * kSp32PLd);
+  float* Ps = Vs + kSp32BK * kSp32Ld;                     // [64 keys][BQ + 4]
+  int* rows = reinterpret_cast<int*>(Ps + kSp32BK * (BQ + 4));
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const int QB = (M + kSp32BQ - 1) / kSp32BQ, QT = (M + HSA_QUERY_TILE - 1) / HSA_QUERY_TILE;
+  const int QB = (M + BQ - 1) / BQ, QT = (M + HSA_QUERY_TILE - 1) / HSA_QUERY_TILE;
   int b = blockIdx.x;
   const int split = b % n_split;
   b /= n_split;
   const int qb = b % QB, h = b / QB;
-  const int D = H * 128, m0 = qb * kSp32BQ;
+  const int D = H * 128, m0 = qb * BQ;
   const size_t unit = (size_t)h * QT + m0 / HSA_QUERY_TILE;
 #pragma unroll
-  for (int i = 0; i < kSp32BQ / 4; ++i) {
-    const int r = (tid >> 5) + 4 * i, c4 = tid & 31;
+  for (int i = 0; i < BQ / kWarps; ++i) {
+    const int r = (tid >> 5) + kWarps * i, c4 = tid & 31;
     const bool ok = m0 + r < M;
     copy16_async(Qs + r * kSp32Ld + 4 * c4, Q + (size_t)(ok ? m0 + r : m0) * D + h * 128 + 4 * c4, ok);
   }
@@ -781,8 +786,8 @@ __global__ void __launch_bounds__(128, 1)
   // the 64 keys from cache row k0, zeros beyond the cache
   auto load_tile = [&](float* dst, const float* src, int k0) {
 #pragma unroll
-    for (int i = 0; i < kSp32BK / 4; ++i) {
-      const int key = (tid >> 5) + 4 * i, c4 = tid & 31;
+    for (int i = 0; i < kSp32BK / kWarps; ++i) {
+      const int key = (tid >> 5) + kWarps * i, c4 = tid & 31;
       const bool ok = k0 + key < L;
       copy16_async(dst + key * kSp32Ld + 4 * c4, src + (size_t)(ok ? k0 + key : 0) * D + h * 128 + 4 * c4, ok);
     }
@@ -812,7 +817,7 @@ __global__ void __launch_bounds__(128, 1)
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
     for (int c = 0; c < 128; c += 4) {
       float4 kk[4];
 #pragma unroll
@@ -860,16 +865,16 @@ __global__ void __launch_bounds__(128, 1)
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float* dst = Ps + (tx + 16 * j) * kSp32PLd + 8 * ty;
+      float* dst = Ps + (tx + 16 * j) * (BQ + 4) + 8 * ty;
       st4(dst, make_float4(p[0][j], p[1][j], p[2][j], p[3][j]));
       st4(dst + 4, make_float4(p[4][j], p[5][j], p[6][j], p[7][j]));
     }
     if (t + 1 < nt) copy_wait<1>();                       // V_t; K_{t+1} may still travel
     else copy_wait<0>();
     __syncthreads();
-#pragma unroll 2
+#pragma unroll 4
     for (int key = 0; key < kSp32BK; ++key) {
-      const float4 pa = ld4(Ps + key * kSp32PLd + 8 * ty), pb = ld4(Ps + key * kSp32PLd + 8 * ty + 4);
+      const float4 pa = ld4(Ps + key * (BQ + 4) + 8 * ty), pb = ld4(Ps + key * (BQ + 4) + 8 * ty + 4);
       const float4 va = ld4(Vs + key * kSp32Ld + 4 * tx), vb = ld4(Vs + key * kSp32Ld + 64 + 4 * tx);
       const float pw[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
       const float2 vv[4] = {make_float2(va.x, va.y), make_float2(va.z, va.w), make_float2(vb.x, vb.y),
@@ -889,7 +894,7 @@ __global__ void __launch_bounds__(128, 1)
   for (int i = 0; i < 8; ++i) {
     const int row = 8 * ty + i, grow = m0 + row;
     if (grow >= M) continue;
-    const size_t slot = (size_t)blockIdx.x * kSp32BQ + row;
+    const size_t slot = (size_t)blockIdx.x * BQ + row;
     const bool whole = n_split == 1;
     const float w = whole ? (l[i] > 0.f ? 1.0f / l[i] : 0.f) : 1.0f;
     float* dst = (whole ? O + (size_t)grow * D + h * 128 : part_o + slot * 128) + 4 * tx;
@@ -901,15 +906,15 @@ __global__ void __launch_bounds__(128, 1)
 
 __global__ void __launch_bounds__(256) k_attn_sparse_f32_combine(const float* __restrict__ part_o,
                                                                  const float2* __restrict__ part_ml, int M, int H,
-                                                                 int n_split, float* __restrict__ O) {
+                                                                 int n_split, int BQ, float* __restrict__ O) {
   pdl_prologue();
   const int w = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  const int QB = (M + kSp32BQ - 1) / kSp32BQ;
-  const int row = w % kSp32BQ, unit = w / kSp32BQ;
+  const int QB = (M + BQ - 1) / BQ;
+  const int row = w % BQ, unit = w / BQ;
   if (unit >= QB * H) return;
-  const int qb = unit % QB, h = unit / QB, grow = qb * kSp32BQ + row;
+  const int qb = unit % QB, h = unit / QB, grow = qb * BQ + row;
   if (grow >= M) return;
-  const float4 o = merge_ranges(part_o, part_ml, (size_t)unit * n_split * kSp32BQ + row, kSp32BQ, n_split, lane,
+  const float4 o = merge_ranges(part_o, part_ml, (size_t)unit * n_split * BQ + row, BQ, n_split, lane,
                                 [](float x) { return expf(x); });
   st4(O + (size_t)grow * (H * 128) + h * 128 + 4 * lane, o);
 }
@@ -931,13 +936,19 @@ TailSplit sparse_plan(int M, int H, int keep, int block) {
   return plan_tail(U, tiles, sms);
 }
 
-// The fp32 kernel's list ranges: one 64-key tile or more each, one CTA per SM, partials within the workspace
-int sparse_f32_splits(int M, int H, int keep, int block, size_t ws_bytes) {
-  const long long units = (long long)((M + kSp32BQ - 1) / kSp32BQ) * H;
+// The fp32 kernel's query rows per CTA: 128 where that, with the lists split, still fills the SMs
+int sparse_f32_rows(int M, int H, int keep) {
+  const long long units = (long long)((M + 127) / 128) * H;
+  return units * (keep < 32 ? keep : 32) >= num_sms() ? 128 : 64;
+}
+
+// Its list ranges: one block or more each, one CTA per SM, partials within the workspace
+int sparse_f32_splits(int M, int H, int keep, int BQ, size_t ws_bytes) {
+  const long long units = (long long)((M + BQ - 1) / BQ) * H;
   long long S = num_sms() / units;
   if (S > keep) S = keep;
   if (S > 32) S = 32;
-  const size_t per = (size_t)units * kSp32BQ * (128 * sizeof(float) + sizeof(float2));
+  const size_t per = (size_t)units * BQ * (128 * sizeof(float) + sizeof(float2));
   if ((size_t)S * per + 256 > ws_bytes) S = ws_bytes < 256 ? 1 : (long long)((ws_bytes - 256) / per);
   return S < 1 ? 1 : (int)S;
 }
@@ -984,25 +995,29 @@ int sparse_f32(const float* Q, int M, const float* K, const float* V, int L, int
                void* ws, size_t ws_bytes, cudaStream_t st) {
   static PerContextOnce attr;
   int rc = attr.ensure([](void**) {
-    if (cudaFuncSetAttribute(k_attn_sparse_f32, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSp32Smem + 4 * HSA_SPARSE_MAX_KEEP) != cudaSuccess)
+    if (cudaFuncSetAttribute(k_attn_sparse_f32<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             sparse_f32_smem(64) + 4 * HSA_SPARSE_MAX_KEEP) != cudaSuccess ||
+        cudaFuncSetAttribute(k_attn_sparse_f32<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             sparse_f32_smem(128) + 4 * HSA_SPARSE_MAX_KEEP) != cudaSuccess)
       return check_launch("sparse attention (fp32): shared-memory attribute");
     return (int)HSA_OK;
   });
   if (rc) return rc;
-  const int QB = (M + kSp32BQ - 1) / kSp32BQ;
-  const int S = ws ? sparse_f32_splits(M, H, sl.keep, sl.block, ws_bytes) : 1;
-  const size_t o_bytes = align256((size_t)QB * H * S * kSp32BQ * 128 * sizeof(float));
+  const int BQ = sparse_f32_rows(M, H, sl.keep), QB = (M + BQ - 1) / BQ;
+  const int S = ws ? sparse_f32_splits(M, H, sl.keep, BQ, ws_bytes) : 1;
+  const size_t o_bytes = align256((size_t)QB * H * S * BQ * 128 * sizeof(float));
   float* part_o = S > 1 ? static_cast<float*>(ws) : nullptr;
   float2* part_ml = S > 1 ? reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + o_bytes) : nullptr;
   ScopedTiming timing(HSA_KCLASS_ATTENTION, st);
-  launch(k_attn_sparse_f32, (unsigned)(QB * H * S), 128, kSp32Smem + 4 * sl.keep, st, Q, M, K, V, L, H, S, sl, O,
-         part_o, part_ml);
+  const unsigned ctas = (unsigned)(QB * H * S);
+  const size_t smem = sparse_f32_smem(BQ) + 4 * (size_t)sl.keep;
+  if (BQ == 128) launch(k_attn_sparse_f32<128>, ctas, 256, smem, st, Q, M, K, V, L, H, S, sl, O, part_o, part_ml);
+  else launch(k_attn_sparse_f32<64>, ctas, 128, smem, st, Q, M, K, V, L, H, S, sl, O, part_o, part_ml);
   count_launch(1);
   rc = check_launch("sparse attention (fp32) launch");
   if (rc || S == 1) return rc;
-  const long long warps = (long long)QB * H * kSp32BQ;
-  launch(k_attn_sparse_f32_combine, (unsigned)((warps + 7) / 8), 256, 0, st, part_o, part_ml, M, H, S, O);
+  const long long warps = (long long)QB * H * BQ;
+  launch(k_attn_sparse_f32_combine, (unsigned)((warps + 7) / 8), 256, 0, st, part_o, part_ml, M, H, S, BQ, O);
   count_launch(1);
   return check_launch("sparse attention (fp32) combine launch");
 }
@@ -1015,9 +1030,9 @@ using namespace hsa;
 extern "C" size_t hsa_sparse_attention_workspace_size(int M, int L, int H, int dtype, int block_k, int keep) {
   if (M <= 0 || L <= 0 || H <= 0 || keep < 1 || keep > HSA_SPARSE_MAX_KEEP || (block_k != 64 && block_k != 128)) return 0;
   if (dtype == HSA_F32) {
-    const int S = sparse_f32_splits(M, H, keep, block_k, ~size_t(0));
+    const int BQ = sparse_f32_rows(M, H, keep), S = sparse_f32_splits(M, H, keep, BQ, ~size_t(0));
     if (S <= 1) return 0;
-    const size_t slots = (size_t)((M + kSp32BQ - 1) / kSp32BQ) * H * S * kSp32BQ;
+    const size_t slots = (size_t)((M + BQ - 1) / BQ) * H * S * BQ;
     return align256(slots * 128 * sizeof(float)) + align256(slots * sizeof(float2)) + 256;
   }
   if (dtype != HSA_BF16) return 0;
