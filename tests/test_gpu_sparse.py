@@ -551,6 +551,61 @@ def test_captured_graph_follows_new_inputs(cuda_lib, M):
     assert hsa.device_status() == 0
 
 
+def test_calls_without_rows_do_nothing(cuda_lib):
+    hsa, bf = cuda_lib, torch.bfloat16
+    q, k = torch.empty((0, 256), dtype=bf, device="cuda"), torch.ones((100, 256), dtype=bf, device="cuda")
+    lists, counts = (torch.empty(s, dtype=torch.int32, device="cuda") for s in ((2, 0, 3), (2, 0)))
+    scores = torch.empty((2, 0, 2), device="cuda")
+    before = hsa.launch_count()
+    hsa.block_scores(q, k, 2, 64, scores)
+    hsa.block_select(scores, 3, lists, counts)
+    hsa.sparse_attention(q, k, k, 2, 64, lists, counts, torch.empty_like(q))
+    X = torch.empty((0, 256), device="cuda")
+    hsa.residual_norm(X, q, out=torch.empty_like(q), pre="layer")
+    assert hsa.launch_count() == before and hsa.device_status() == 0
+
+
+def test_binding_refuses_mixed_devices_types_and_shapes(cuda_lib):
+    hsa, bf = cuda_lib, torch.bfloat16
+    q, k = torch.ones((130, 256), dtype=bf, device="cuda"), torch.ones((100, 256), dtype=bf, device="cuda")
+    scores = torch.empty((2, 2, 2), device="cuda")
+    with pytest.raises(ValueError, match="shape"):
+        hsa.block_scores(q, k, 2, 64, scores[:, :1])
+    with pytest.raises(ValueError, match="device"):
+        hsa.block_scores(q, k.cpu(), 2, 64, scores)
+    with pytest.raises(TypeError):
+        hsa.block_scores(q, k.float(), 2, 64, scores)
+    with pytest.raises(ValueError, match="block"):
+        hsa.block_scores(q, k, 2, 32, scores)
+    with pytest.raises(ValueError, match="device"):
+        hsa.block_scores(q, k, 2, 64, scores, ws=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(hsa.HsaError):
+        hsa.block_scores(q, k, 2, 64, scores, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    lists, counts = torch.zeros((2, 2, 3), dtype=torch.int32, device="cuda"), torch.zeros((2, 2), dtype=torch.int32,
+                                                                                          device="cuda")
+    with pytest.raises(ValueError, match="shape"):
+        hsa.block_select(scores, 4, lists, counts)
+    with pytest.raises(TypeError):
+        hsa.block_select(scores, 3, lists, counts.long())
+    with pytest.raises(ValueError, match="shape"):
+        hsa.block_select(scores, 3, lists, counts, forced=torch.zeros(3, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="contiguous"):
+        hsa.sparse_attention(q, k, torch.ones((256, 100), dtype=bf, device="cuda").t(), 2, 64, lists, counts,
+                             torch.empty_like(q))
+    with pytest.raises(hsa.HsaError):
+        hsa.sparse_attention(q, k, k, 2, 96, lists, counts, torch.empty_like(q))
+    X, tab = torch.zeros((130, 256), device="cuda"), torch.zeros((4, 3, 256), device="cuda")
+    with pytest.raises(ValueError, match="mod_row"):
+        hsa.residual_norm(X, q, gate=tab[:, 0])
+    with pytest.raises(ValueError, match="stride"):
+        hsa.residual_norm(X, q, gate=tab[0, 0], pre="rms", out=q, mul=tab[:, 1])
+    with pytest.raises(ValueError, match="rows of"):
+        hsa.residual_norm(X, q, gate=tab[0, 0].bfloat16())
+    with pytest.raises(hsa.HsaError):
+        hsa.residual_norm(X, q, out=q.clone())             # an output without a norm
+    assert hsa.device_status() == 0
+
+
 def test_calls_use_the_stream_they_are_given(cuda_lib):
     """Inputs written late on a side stream: calls given that stream wait for them."""
     hsa, M, N, H = cuda_lib, 200, 600, 1
