@@ -419,8 +419,20 @@ def gated_residual(X, y, b=None, gate=None, stream=None):
 # A call of these operators takes the GPU a few microseconds, so the checks of their arguments are kept
 # to a few comparisons each; _refuse says what is wrong once one has failed.
 
+_torch = None
+_codes: dict = {}
+
+
+def _use_torch():
+    global _torch
+    import torch
+    _codes.update({torch.bfloat16: HSA_BF16, torch.float32: HSA_F32})
+    _torch = torch
+    return torch
+
+
 def _bad(t, shape, dtype, dev: int) -> bool:
-    return not (t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev)
+    return t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev
 
 
 def _refuse(t, name, shape, dtype, dev: int):
@@ -430,12 +442,16 @@ def _refuse(t, name, shape, dtype, dev: int):
     raise ValueError(f"{name} must be on the device of the first operand, got {t.device}")
 
 
+def _code_of(t) -> int:
+    code = _codes.get(t.dtype)
+    return _dtype_code(t) if code is None else code       # which refuses the type
+
+
 def _current(dev: int, stream) -> int:
     """The stream handle of a call on tensors of device `dev`, which has to be the current one."""
-    import torch
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != _torch._C._cuda_getDevice():
         raise ValueError(f"the operands must be on the current CUDA device, got device {dev}")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _block_count(n: int, size: int) -> int:
@@ -449,12 +465,12 @@ def block_scores_workspace_size(M: int, L: int, H: int, block: int) -> int:
 def block_scores(q, k, H: int, block: int, scores, ws=None, stream=None):
     """scores[h, t, b] = mean logit of query tile t (128 rows of q) against block b (`block` rows of k),
     float32 (hsa_block_scores); `ws`: uint8, at least block_scores_workspace_size bytes."""
-    import torch
+    torch = _torch or _use_torch()
     M, L, D, dt, dev = q.shape[0], k.shape[0], H * 128, q.dtype, q.get_device()
-    code = _dtype_code(q)
-    if block not in (64, 128):
+    code = _code_of(q)
+    if block != 64 and block != 128:
         raise ValueError("block must be 64 or 128")
-    out = (H, _block_count(M, QUERY_TILE), _block_count(L, block))
+    out = (H, (M + QUERY_TILE - 1) // QUERY_TILE, (L + block - 1) // block)
     if _bad(q, (M, D), dt, dev): _refuse(q, "q", (M, D), dt, dev)
     if _bad(k, (L, D), dt, dev): _refuse(k, "k", (L, D), dt, dev)
     if _bad(scores, out, torch.float32, dev): _refuse(scores, "scores", out, torch.float32, dev)
@@ -463,14 +479,16 @@ def block_scores(q, k, H: int, block: int, scores, ws=None, stream=None):
         ws = torch.empty(block_scores_workspace_size(M, L, H, block), dtype=torch.uint8, device=q.device)
     elif ws.get_device() != dev:
         raise ValueError("ws must be on the operands' device")
-    _check(lib().hsa_block_scores(q.data_ptr(), M, k.data_ptr(), L, H, code, block, scores.data_ptr(), ws.data_ptr(),
-                                  ws.numel() * ws.element_size(), st), "hsa_block_scores")
+    rc = (_lib or load()).hsa_block_scores(q.data_ptr(), M, k.data_ptr(), L, H, code, block, scores.data_ptr(),
+                                           ws.data_ptr(), ws.nbytes, st)
+    if rc:
+        raise HsaError(rc, "hsa_block_scores")
 
 
 def block_select(scores, keep: int, lists, counts, forced=None, stream=None):
     """The `keep` best blocks of every score row (hsa_block_select): scores (..., blocks) float32 ->
     lists (..., keep) and counts (...) int32; `forced` (uint8 [blocks], optional) rank ahead."""
-    import torch
+    torch = _torch or _use_torch()
     shape, dev = scores.shape, scores.get_device()
     lead, B, i32t = shape[:-1], shape[-1], torch.int32
     if _bad(scores, shape, torch.float32, dev): _refuse(scores, "scores", shape, torch.float32, dev)
@@ -478,8 +496,11 @@ def block_select(scores, keep: int, lists, counts, forced=None, stream=None):
     if _bad(counts, lead, i32t, dev): _refuse(counts, "counts", lead, i32t, dev)
     if forced is not None and _bad(forced, (B,), torch.uint8, dev): _refuse(forced, "forced", (B,), torch.uint8, dev)
     st = _current(dev, stream)
-    _check(lib().hsa_block_select(scores.data_ptr(), counts.numel(), B, keep, _ptr(forced), lists.data_ptr(),
-                                  counts.data_ptr(), st), "hsa_block_select")
+    rc = (_lib or load()).hsa_block_select(scores.data_ptr(), counts.numel(), B, keep,
+                                           None if forced is None else forced.data_ptr(), lists.data_ptr(),
+                                           counts.data_ptr(), st)
+    if rc:
+        raise HsaError(rc, "hsa_block_select")
 
 
 def sparse_attention_workspace_size(M: int, L: int, H: int, dtype: int, block: int, keep: int) -> int:
@@ -491,10 +512,10 @@ def sparse_attention(q, k, v, H: int, block: int, lists, counts, o, stream=None,
     tile (hsa_sparse_attention): lists (H, tiles, keep), counts (H, tiles) int32 as block_select writes
     them; with `ws` (uint8, at least sparse_attention_workspace_size bytes) long lists of few rows are
     split."""
-    import torch
+    torch = _torch or _use_torch()
     M, L, D, dt, dev = q.shape[0], k.shape[0], H * 128, q.dtype, q.get_device()
-    code, keep, i32t = _dtype_code(q), lists.shape[-1], torch.int32
-    T = _block_count(M, QUERY_TILE)
+    code, keep, i32t = _code_of(q), lists.shape[-1], torch.int32
+    T = (M + QUERY_TILE - 1) // QUERY_TILE
     if _bad(q, (M, D), dt, dev): _refuse(q, "q", (M, D), dt, dev)
     if _bad(k, (L, D), dt, dev): _refuse(k, "k", (L, D), dt, dev)
     if _bad(v, (L, D), dt, dev): _refuse(v, "v", (L, D), dt, dev)
@@ -504,10 +525,12 @@ def sparse_attention(q, k, v, H: int, block: int, lists, counts, o, stream=None,
     if ws is not None and ws.get_device() != dev:
         raise ValueError("ws must be on the operands' device")
     st = _current(dev, stream)
-    _check(lib().hsa_sparse_attention(q.data_ptr(), M, k.data_ptr(), v.data_ptr(), L, H, code, block,
-                                      lists.data_ptr(), keep, counts.data_ptr(), o.data_ptr(), _ptr(ws),
-                                      0 if ws is None else ws.numel() * ws.element_size(), st),
-           "hsa_sparse_attention")
+    rc = (_lib or load()).hsa_sparse_attention(q.data_ptr(), M, k.data_ptr(), v.data_ptr(), L, H, code, block,
+                                               lists.data_ptr(), keep, counts.data_ptr(), o.data_ptr(),
+                                               None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
+                                               st)
+    if rc:
+        raise HsaError(rc, "hsa_sparse_attention")
 
 
 # ---------------------------------------------------------------- residual update fused with its norms
@@ -522,13 +545,13 @@ def residual_norm(X, y, X_out=None, out=None, b=None, post="none", post_g=None, 
     when not `modulate` (hsa_residual_norm).  post, pre: "none", "rms" or "layer"; X_out defaults to X.
     gate, mul, add: [D], or (n_mod, D) views of one modulation table (equal row strides) whose row is
     mod_row[token], token = idx[r] (idx None: r)."""
-    import torch
+    torch = _torch or _use_torch()
     shape, f32t, dev = X.shape, torch.float32, X.get_device()
     M, D = shape
     if post not in _NORMS or pre not in _NORMS:
         raise ValueError("post and pre must be 'none', 'rms' or 'layer'")
     X_out = X if X_out is None else X_out
-    y_code, out_code = _dtype_code(y), HSA_F32 if out is None else _dtype_code(out)
+    y_code, out_code = _code_of(y), HSA_F32 if out is None else _code_of(out)
     if X.dtype is not f32t or not X.is_contiguous(): _refuse(X, "X", shape, f32t, dev)
     if X_out is not X and _bad(X_out, shape, f32t, dev): _refuse(X_out, "X_out", shape, f32t, dev)
     if y.shape != shape or not y.is_contiguous() or y.get_device() != dev: _refuse(y, "y", shape, y.dtype, dev)
@@ -569,7 +592,9 @@ def residual_norm(X, y, X_out=None, out=None, b=None, post="none", post_g=None, 
         0 if post_b is None else post_b.data_ptr(), 0 if gate is None else gate.data_ptr(),
         0 if mul is None else mul.data_ptr(), 0 if add is None else add.data_ptr(), 1 if modulate else 0, res_scale,
         0 if mod_row is None else mod_row.data_ptr(), 0 if idx is None else idx.data_ptr(), N, n_mod or 1, step or D)
-    _check(lib().hsa_residual_norm(a, st), "hsa_residual_norm")
+    rc = (_lib or load()).hsa_residual_norm(a, st)
+    if rc:
+        raise HsaError(rc, "hsa_residual_norm")
 
 
 class HostSlot:
