@@ -16,9 +16,10 @@
 // shared memory, filled by bulk copies (one elected lane, an mbarrier per slot), so the next row's X
 // and y travel while this row is reduced and written; the copies bypass L1, which keeps the
 // modulation vectors that neighbouring rows share.
-// Measured, 32760 x 1536 (bf16 in and out) / 8190 x 5120 (float32 in, bf16 out): 103 / 97 us, 5.8 / 6.0 TB/s
-// of the 6.56 a copy reaches; 16 warps of 48 values a thread 111 / 102, 8 warps 127 / 119; a warp per row
-// with plain loads and no ring 150 / 122.
+// Measured, 32760 x 1536 (bf16 in and out) / 8190 x 5120 (float32 in, bf16 out), one set of buffers again and
+// again: 103 / 97 us; 16 warps of 48 values a thread 111 / 102, 8 warps 127 / 119; a warp per row with plain
+// loads and no ring 150 / 122.  With sets that take turns, so that nothing is left in L2: 108 / 107 us, 5.6 /
+// 5.5 TB/s of the 6.56 a copy reaches; cache hints on the loads or stores and larger rings change that by 2 % at most.
 #include "common.cuh"
 
 namespace hsa {
