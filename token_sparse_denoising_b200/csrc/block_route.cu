@@ -359,7 +359,8 @@ constexpr int kRouteFew = 32;      // keys a warp ranks against each other to fi
 // interval, which bounds the passes whatever the scores.  Once at most 32 keys are left between the
 // bounds, a warp with many registers of keys moves them to one register a lane and ranks them.
 // Then the chosen blocks are written in index order.  Bound by instructions: a row of 1182 scores
-// takes a warp about 1500, against 4.7 KB read.
+// takes a warp about 3100, against 4.7 KB read (80 us for 23640 such rows; 309 by halving from keys loaded one
+// by one).
 template <int W, int V>
 __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, W == 1 ? (V > 16 ? 3 : 4) : (V > 40 ? 8 : 24) / W)
     k_block_select(const float* __restrict__ scores, int rows, int n_blocks, int keep,
@@ -623,10 +624,12 @@ extern "C" int hsa_block_scores(const void* d_q, int M, const void* d_k, int L, 
   rc = make_tmap_2d(&ta, means, true, (uint64_t)H * 128, planes, (uint64_t)H * 256, 64, 128, true);
   if (!rc) rc = make_tmap_2d(&tb, means, true, (uint64_t)H * 128, planes, (uint64_t)H * 256, 64, 64, true);
   if (rc) return rc;
-  // ranges of block tiles: as many CTAs as SMs while a head's 128 query tiles leave some idle, else ranges
-  // of about six tiles (the query side is loaded once per range)
-  const int tiles_b = blocks_of(B, 64), units = blocks_of(T, 128) * H;
-  int ranges = num_sms() / units > blocks_of(tiles_b, 6) ? num_sms() / units : blocks_of(tiles_b, 6);
+  // ranges of block tiles: as many CTAs as SMs while a head's 128 query tiles leave some idle (one range a
+  // head: 48.8 against 42.8 us for the whole call at 32760 x 32760, 12 heads), else ranges of about twelve
+  // tiles, the query side being loaded once per range (three / six / twelve: 366 / 354 / 345 us at 75600 x
+  // 75600, 40 heads)
+  const int tiles_b = blocks_of(B, 64), units = blocks_of(T, 128) * H, few = blocks_of(tiles_b, 12);
+  int ranges = num_sms() / units > few ? num_sms() / units : few;
   ranges = ranges > tiles_b ? tiles_b : ranges;
   launch(k_block_product, dim3((unsigned)ranges, (unsigned)blocks_of(T, 128), (unsigned)H), 192, kProdSmem, st, ta, tb,
          T, B, d_scores);
