@@ -551,6 +551,49 @@ def test_captured_graph_follows_new_inputs(cuda_lib, M):
     assert hsa.device_status() == 0
 
 
+def test_two_streams_at_once(cuda_lib):
+    """The same calls on two streams with their own buffers, started together, give what they give alone."""
+    hsa, bf, H, N, block, keep = cuda_lib, torch.bfloat16, 2, 6000, 64, 20
+    sets = []
+    for i in range(2):
+        M = (2100, 700)[i]
+        a, b, c = qkv(130 + i, M, N, H, True)
+        d = dict(q=dev(a, bf), k=dev(b, bf), v=dev(c, bf), scores=torch.empty((H, cdiv(M, 128), cdiv(N, block)),
+                                                                                device="cuda"),
+                 lists=torch.empty((H, cdiv(M, 128), keep), dtype=torch.int32, device="cuda"),
+                 counts=torch.empty((H, cdiv(M, 128)), dtype=torch.int32, device="cuda"),
+                 X=torch.zeros((M, 256), device="cuda"), stream=torch.cuda.Stream(),
+                 sws=torch.empty(hsa.block_scores_workspace_size(M, N, H, block), dtype=torch.uint8, device="cuda"),
+                 ws=torch.empty(hsa.sparse_attention_workspace_size(M, N, H, hsa.HSA_BF16, block, keep),
+                                dtype=torch.uint8, device="cuda"))
+        d["o"] = torch.empty_like(d["q"])
+        sets.append(d)
+
+    def calls(d, stream):
+        hsa.block_scores(d["q"], d["k"], H, block, d["scores"], ws=d["sws"], stream=stream)
+        hsa.block_select(d["scores"], keep, d["lists"], d["counts"], stream=stream)
+        hsa.sparse_attention(d["q"], d["k"], d["v"], H, block, d["lists"], d["counts"], d["o"], ws=d["ws"],
+                             stream=stream)
+        hsa.residual_norm(d["X"], d["o"], post="rms", stream=stream)
+
+    want = []
+    for d in sets:
+        calls(d, None)
+        torch.cuda.synchronize()
+        want.append((d["o"].clone(), d["X"].clone()))
+    for _ in range(5):
+        for d in sets:
+            d["o"].fill_(float("nan"))
+            d["X"].zero_()
+        torch.cuda.synchronize()
+        for d in sets:
+            calls(d, d["stream"])
+        torch.cuda.synchronize()
+        for d, (o, X) in zip(sets, want):
+            assert torch.equal(d["o"], o) and torch.equal(d["X"], X)
+    assert hsa.device_status() == 0
+
+
 def test_calls_without_rows_do_nothing(cuda_lib):
     hsa, bf = cuda_lib, torch.bfloat16
     q, k = torch.empty((0, 256), dtype=bf, device="cuda"), torch.ones((100, 256), dtype=bf, device="cuda")

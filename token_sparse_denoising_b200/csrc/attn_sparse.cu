@@ -21,7 +21,8 @@
 // per tile.  V has one slot per parity: the producer's arrival on p_full[b] for tile g follows its wait for
 // the slot, which the MMA warp releases after it has waited for both halves of P_{g-2}; so no arrival lands
 // a phase early, whatever the unit boundaries.  The softmax warpgroups take the registers that the control
-// warpgroup gives up (208 + 208 + 88 = 3 x 168 a thread at launch; 56 or 72 for the control warps spill or are 1 % slower).
+// warpgroup gives up (208 + 208 + 88 = 3 x 168 a thread at launch; 56 or 72 for the control warps spill or
+// are 1 % slower, and spills in the softmax, as with all of O in registers at once, cost 15 %).
 // A tile's 128 keys are one listed 128-row block (two 64-column boxes) or two listed 64-row blocks (four
 // 64 x 64 boxes), so a finer list costs only more TMA instructions, and the tensor-core shapes stay
 // 128 x 128 x 128.  A unit's list is staged in shared memory as 16-bit block numbers; kNoBlock stands for
@@ -30,7 +31,7 @@
 // last block may stand anywhere in a list).
 //
 // Rounding: logits, running max and sum, and O are float32; p is rounded to bf16 for the second
-// product (its sum is taken before the rounding, relative error 2^-9 per term), and O once at the end.
+// product (its sum is taken before the rounding; at most 2^-8 of each term), and O once at the end.
 #include "tcgen05.cuh"
 
 namespace hsa {
