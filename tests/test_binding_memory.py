@@ -1,0 +1,99 @@
+"""Memory that the binding takes or is given, on the CPU: whose stream a call's own scratch belongs to, and
+buffers that a kernel could not use as they are.  A recorder stands in for libhsa; nothing is launched."""
+import contextlib
+
+import pytest
+import torch
+
+from token_sparse_denoising_b200 import hsa
+
+
+class Recorder:
+    """Every function of the library: notes its name and arguments and returns 0, or a size that is set."""
+
+    def __init__(self, **sizes):
+        self.sizes, self.calls = sizes, []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return self.sizes.get(name, 0)
+        return call
+
+    def launches(self):
+        return [c for c in self.calls if not c[0].endswith("_size")]
+
+
+class Stream:
+    cuda_stream = 77
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """The stream that is current while each tensor is allocated, in order (None: the caller's own)."""
+    current, seen = [None], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        current.append(s)
+        yield
+        current.pop()
+
+    def empty(*args, _empty=torch.empty, **kw):
+        seen.append(current[-1])
+        return _empty(*args, **kw)
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream())
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(hsa, "_current", lambda dev, s: 0 if s is None else s.cuda_stream)
+    return seen
+
+
+def use(monkeypatch, **sizes):
+    lib = Recorder(**sizes)
+    monkeypatch.setattr(hsa, "_lib", lib)
+    return lib
+
+
+@pytest.mark.parametrize("side", [True, False])
+def test_block_scores_takes_its_scratch_on_the_calls_stream(monkeypatch, streams, side):
+    lib = use(monkeypatch, hsa_block_scores_workspace_size=4096)
+    q, k, scores = torch.zeros(300, 256), torch.zeros(1000, 256), torch.zeros(2, 3, 16)
+    s = Stream() if side else None
+    hsa.block_scores(q, k, 2, 64, scores, stream=s)
+    assert streams == [s] and [c[0] for c in lib.launches()] == ["hsa_block_scores"]
+    assert lib.launches()[0][1][-1] == (77 if side else 0)
+
+
+@pytest.mark.gpu
+def test_block_scores_on_a_side_stream_keep_their_scratch(cuda_lib):
+    """Scratch of a call that waits on a side stream is not handed out meanwhile, nor taken from memory that
+    the current stream still uses: the scores are the current stream's own, and so is the other tensor."""
+    M, L, H, block = 2000, 3000, 4, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    q, k = (torch.randn((n, 128 * H), generator=g, device="cuda").bfloat16() for n in (M, L))
+    want, got = (torch.empty((H, 16, 47), device="cuda") for _ in range(2))
+    n = cuda_lib.block_scores_workspace_size(M, L, H, block)
+    cuda_lib.block_scores(q, k, H, block, want)
+    side = torch.cuda.Stream()
+    for late in (True, False):
+        got.fill_(float("nan"))
+        torch.cuda.synchronize()
+        if late:                                          # the call waits, the current stream goes on
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(20_000_000)
+            cuda_lib.block_scores(q, k, H, block, got, stream=side)
+            others = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        else:                                             # the current stream still writes what it has given back
+            torch.cuda._sleep(20_000_000)
+            others = [torch.full((n,), 255, dtype=torch.uint8, device="cuda")]
+            kept = others[0].clone()
+            del others[0]
+            cuda_lib.block_scores(q, k, H, block, got, stream=side)
+            others = [kept]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        assert all(bool((t == 255).all()) for t in others)
+    assert cuda_lib.device_status() == 0

@@ -150,6 +150,16 @@ def _stream(stream=None):
     return s.cuda_stream
 
 
+def _scratch(nbytes: int, device, stream=None):
+    """Scratch of one call on `stream` (None: the current one).  It is taken from that stream's memory, so
+    whatever the allocator gives it to next runs behind the call's kernels."""
+    import torch
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _dtype_code(t) -> int:
     import torch
     if t.dtype == torch.bfloat16:
@@ -476,7 +486,7 @@ def block_scores(q, k, H: int, block: int, scores, ws=None, stream=None):
     if _bad(scores, out, torch.float32, dev): _refuse(scores, "scores", out, torch.float32, dev)
     st = _current(dev, stream)
     if ws is None:
-        ws = torch.empty(block_scores_workspace_size(M, L, H, block), dtype=torch.uint8, device=q.device)
+        ws = _scratch(block_scores_workspace_size(M, L, H, block), q.device, stream)
     elif ws.get_device() != dev:
         raise ValueError("ws must be on the operands' device")
     rc = (_lib or load()).hsa_block_scores(q.data_ptr(), M, k.data_ptr(), L, H, code, block, scores.data_ptr(),
