@@ -66,6 +66,16 @@ def test_block_scores_takes_its_scratch_on_the_calls_stream(monkeypatch, streams
     assert lib.launches()[0][1][-1] == (77 if side else 0)
 
 
+@pytest.mark.parametrize("side", [True, False])
+@pytest.mark.parametrize("pinned", [True, False])
+def test_select_tokens_takes_its_scratch_on_the_calls_stream(monkeypatch, streams, side, pinned):
+    lib = use(monkeypatch, hsa_select_tokens_workspace_size=512)
+    s = Stream() if side else None
+    hsa.select_tokens(torch.zeros(100), [40, 60], torch.zeros(100, dtype=torch.int8), torch.zeros(100, dtype=torch.int32),
+                      stream=s, pinned=torch.zeros(100, dtype=torch.uint8) if pinned else None)
+    assert streams == [s] and len(lib.launches()) == 1 and lib.launches()[0][1][-1] == 77
+
+
 @pytest.mark.gpu
 def test_block_scores_on_a_side_stream_keep_their_scratch(cuda_lib):
     """Scratch of a call that waits on a side stream is not handed out meanwhile, nor taken from memory that

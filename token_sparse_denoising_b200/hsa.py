@@ -242,7 +242,7 @@ def select_tokens(score, group_sizes, group, order, stream=None, ws=None, pinned
     sizes = np.ascontiguousarray(group_sizes, np.int32)
     nbytes = lib().hsa_select_tokens_workspace_size(N, K)
     if ws is None:
-        ws = torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=score.device)
+        ws = _scratch(max(int(nbytes), 1), score.device, stream)
     elif ws.numel() * ws.element_size() < nbytes:
         raise ValueError("select_tokens: workspace smaller than hsa_select_tokens_workspace_size")
     if pinned is None:
