@@ -1,11 +1,12 @@
 """Memory that the binding takes or is given, on the CPU: whose stream a call's own scratch belongs to, and
 buffers that a kernel could not use as they are.  A recorder stands in for libhsa; nothing is launched."""
 import contextlib
+import types
 
 import pytest
 import torch
 
-from token_sparse_denoising_b200 import hsa
+from token_sparse_denoising_b200 import hsa, pipeline
 
 
 class Recorder:
@@ -74,6 +75,32 @@ def test_select_tokens_takes_its_scratch_on_the_calls_stream(monkeypatch, stream
     hsa.select_tokens(torch.zeros(100), [40, 60], torch.zeros(100, dtype=torch.int8), torch.zeros(100, dtype=torch.int32),
                       stream=s, pinned=torch.zeros(100, dtype=torch.uint8) if pinned else None)
     assert streams == [s] and len(lib.launches()) == 1 and lib.launches()[0][1][-1] == 77
+
+
+class Elsewhere:
+    """As much of a device tensor as a check looks at."""
+    is_cuda, device, shape = True, torch.device("cuda", 1), (5,)
+
+
+def test_forced_blocks_have_to_be_on_the_steps_device(monkeypatch):
+    """The layer step hands their address on: a CPU tensor's would be read by the kernel, another GPU's too."""
+    lib = use(monkeypatch)
+    mask = torch.ones(5, dtype=torch.uint8)
+    idx, cache = torch.arange(4, dtype=torch.int32), torch.zeros(300, 256)
+    w = types.SimpleNamespace(c=hsa.LayerWeightsC())
+    monkeypatch.setattr(hsa, "_stream", lambda s: 0)
+    with pytest.raises(ValueError, match="device"):
+        hsa.layer_step(w, cache, cache, cache, idx, idx, cache, sparsity=hsa.BlockSparsity(4, 64, mask))
+    with pytest.raises(ValueError, match="device"):
+        pipeline._step_workspace(300, 256, 512, hsa.HSA_BF16, hsa.BlockSparsity(4, 64, mask))
+    monkeypatch.setattr(hsa, "_need", lambda *a: None)
+    monkeypatch.setattr(hsa, "_ptr", lambda t: None)
+    sp = hsa.BlockSparsity(4, 64, Elsewhere())
+    sp.check(300)
+    sp.check(300, torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="device"):
+        sp.check(300, torch.device("cuda", 0))
+    assert not lib.launches()
 
 
 @pytest.mark.gpu

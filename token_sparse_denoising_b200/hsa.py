@@ -329,9 +329,15 @@ class BlockSparsity:
         self.keep, self.block, self.forced = keep, block, forced
         self.c = BlockSparsityC(block, keep, _ptr(forced))
 
-    def check(self, N: int):
-        if self.forced is not None and self.forced.shape != (_block_count(N, self.block),):
+    def check(self, N: int, device=None):
+        """Refuses a `forced` that a step on N tokens, on `device` (None: any GPU), could not read."""
+        f = self.forced
+        if f is None:
+            return
+        if f.shape != (_block_count(N, self.block),):
             raise ValueError(f"forced must have one entry per block of {self.block} of the {N} tokens")
+        if not f.is_cuda or (device is not None and f.device != device):
+            raise ValueError(f"forced must be on the device of the step, got {f.device}")
 
 
 def layer_step_workspace_size(M: int, D: int, F: int, dtype: int, N: int | None = None,
@@ -348,7 +354,7 @@ def layer_step(w: "LayerWeights", kcache, vcache, xA, idx, pos, ws, x_src=None, 
     M = idx.shape[0]
     L = 0 if ctx_k is None else ctx_k.shape[0]
     if sparsity is not None:
-        sparsity.check(N)
+        sparsity.check(N, kcache.device)
         _check(lib().hsa_layer_step_sparse(C.byref(w.c), _ptr(kcache), _ptr(vcache), N, _ptr(xA), _ptr(x_src),
                                            _ptr(idx), M, _ptr(pos), _ptr(ctx_k), _ptr(ctx_v), L,
                                            C.byref(sparsity.c), _ptr(ws), ws.numel() * ws.element_size(),

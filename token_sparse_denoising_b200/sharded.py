@@ -162,7 +162,7 @@ class HeadParallelBlock:
         self.ctx_k = self.ctx_v = None
         self.sparsity = sparsity
         if sparsity is not None:
-            sparsity.check(N)
+            sparsity.check(N, self.kc.device)
             h, block = len(shard.heads), sparsity.block
             tiles, blocks = -(-shard.M // hsa.QUERY_TILE), -(-N // block)
             self.scores = torch.empty((h, tiles, blocks), dtype=torch.float32, device=device)
