@@ -103,6 +103,16 @@ def test_forced_blocks_have_to_be_on_the_steps_device(monkeypatch):
     assert not lib.launches()
 
 
+@pytest.mark.parametrize("name,value", [("keep", 8), ("block", 128), ("forced", torch.zeros(5, dtype=torch.uint8))])
+def test_block_sparsity_does_not_change_behind_its_struct(name, value):
+    """The layer step reads the C struct: an attribute set later would leave it with the old numbers, and with
+    the address of a mask that may have been freed."""
+    sp = hsa.BlockSparsity(4, 64, torch.ones(5, dtype=torch.uint8))
+    with pytest.raises(AttributeError):
+        setattr(sp, name, value)
+    assert (sp.c.keep, sp.c.block_k, sp.c.d_forced) == (sp.keep, sp.block, sp.forced.data_ptr())
+
+
 @pytest.mark.gpu
 def test_block_scores_on_a_side_stream_keep_their_scratch(cuda_lib):
     """Scratch of a call that waits on a side stream is not handed out meanwhile, nor taken from memory that

@@ -318,7 +318,8 @@ def context_kv_noalloc(ctx, w_kv2, b_kv2, g_k2, k2, v2, stream=None):
 class BlockSparsity:
     """Block-sparse self-attention of a layer step (hsa_layer_step_sparse): per tile of 128 active rows and
     head the `keep` best-scoring blocks of `block` cache rows; `forced` (uint8 [blocks] on the device,
-    optional: pipeline.forced_blocks) are listed ahead of all others."""
+    optional: pipeline.forced_blocks) are listed ahead of all others.  The contents of `forced` may change
+    between steps; the three attributes may not (workspaces and recordings are made for them)."""
 
     def __init__(self, keep: int, block: int = 64, forced=None):
         import torch
@@ -326,8 +327,12 @@ class BlockSparsity:
             raise ValueError("block must be 64 or 128 and keep in 1..4096")
         if forced is not None:
             _need(forced, "forced", torch.uint8)
-        self.keep, self.block, self.forced = keep, block, forced
+        self._keep, self._block, self._forced = keep, block, forced
         self.c = BlockSparsityC(block, keep, _ptr(forced))
+
+    keep = property(lambda self: self._keep)
+    block = property(lambda self: self._block)
+    forced = property(lambda self: self._forced)
 
     def check(self, N: int, device=None):
         """Refuses a `forced` that a step on N tokens, on `device` (None: any GPU), could not read."""
