@@ -113,6 +113,32 @@ def test_block_sparsity_does_not_change_behind_its_struct(name, value):
     assert (sp.c.keep, sp.c.block_k, sp.c.d_forced) == (sp.keep, sp.block, sp.forced.data_ptr())
 
 
+GAPS = torch.zeros(1 << 16, dtype=torch.uint8)[::2]
+W = types.SimpleNamespace(c=hsa.LayerWeightsC())
+I32 = dict(dtype=torch.int32)
+
+
+@pytest.mark.parametrize("call", [
+    lambda x, v, i: hsa.block_scores(x, x, 2, 64, torch.zeros(2, 3, 5), ws=GAPS),
+    lambda x, v, i: hsa.sparse_attention(x, x, x, 2, 64, torch.zeros(2, 3, 4, **I32), torch.zeros(2, 3, **I32), x, ws=GAPS),
+    lambda x, v, i: hsa.select_tokens(v, [300], i, i, ws=GAPS),
+    lambda x, v, i: hsa.attention(x, x, x, 2, x, ws=GAPS),
+    lambda x, v, i: hsa.context_kv(x, x, v, v, x, x, GAPS),
+    lambda x, v, i: hsa.layer_step(W, x, x, x, i, i, GAPS),
+    lambda x, v, i: hsa.layer_step(W, x, x, x, i, i, GAPS, sparsity=hsa.BlockSparsity(4)),
+    lambda x, v, i: hsa.patch_embed(x, i, x, v, x, GAPS),
+    lambda x, v, i: hsa.velocity_head(x, v, x, v, x, GAPS),
+    lambda x, v, i: hsa.iteration_host(W, x, x, i, i, x, x, 0.1, x, x, types.SimpleNamespace(c=hsa.HostSlotC()), GAPS),
+    lambda x, v, i: hsa.iteration_host(W, x, x, i, i, x, x, 0.1, x, x, types.SimpleNamespace(c=hsa.HostSlotC()), v,
+                                       sel_ws=GAPS)])
+def test_workspaces_without_gaps(monkeypatch, streams, call):
+    """The kernels write `bytes of ws` consecutive bytes: in a strided view they would run over what lies between."""
+    lib = use(monkeypatch)
+    with pytest.raises(ValueError, match="ws must be contiguous"):
+        call(torch.zeros(300, 256), torch.zeros(300), torch.zeros(300, **I32))
+    assert not lib.launches()
+
+
 @pytest.mark.gpu
 def test_block_scores_on_a_side_stream_keep_their_scratch(cuda_lib):
     """Scratch of a call that waits on a side stream is not handed out meanwhile, nor taken from memory that

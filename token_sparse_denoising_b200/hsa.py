@@ -150,6 +150,13 @@ def _stream(stream=None):
     return s.cuda_stream
 
 
+def _ws_bytes(ws) -> int:
+    """Bytes of a caller's workspace, which the kernels write from its address on: one without gaps."""
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.nbytes
+
+
 def _scratch(nbytes: int, device, stream=None):
     """Scratch of one call on `stream` (None: the current one).  It is taken from that stream's memory, so
     whatever the allocator gives it to next runs behind the call's kernels."""
@@ -243,7 +250,7 @@ def select_tokens(score, group_sizes, group, order, stream=None, ws=None, pinned
     nbytes = lib().hsa_select_tokens_workspace_size(N, K)
     if ws is None:
         ws = _scratch(max(int(nbytes), 1), score.device, stream)
-    elif ws.numel() * ws.element_size() < nbytes:
+    elif _ws_bytes(ws) < nbytes:
         raise ValueError("select_tokens: workspace smaller than hsa_select_tokens_workspace_size")
     if pinned is None:
         _check(lib().hsa_select_tokens(_ptr(score), N, K, sizes.ctypes.data, _ptr(group), _ptr(order), _ptr(ws),
@@ -289,7 +296,7 @@ def attention(q, k, v, H: int, o, stream=None, ws=None):
                                    _stream(stream)), "hsa_attention")
     else:
         _check(lib().hsa_attention_ws(_ptr(q), q.shape[0], _ptr(k), _ptr(v), k.shape[0], H, _dtype_code(q),
-                                      _ptr(o), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+                                      _ptr(o), _ptr(ws), _ws_bytes(ws), _stream(stream)),
                "hsa_attention_ws")
 
 
@@ -304,7 +311,7 @@ def context_kv_workspace_size(L: int, D: int) -> int:
 def context_kv(ctx, w_kv2, b_kv2, g_k2, k2, v2, ws, stream=None):
     L, D = ctx.shape
     _check(lib().hsa_context_kv(_ptr(ctx), L, D, _dtype_code(ctx), _ptr(w_kv2), _ptr(b_kv2), _ptr(g_k2), _ptr(k2),
-                                _ptr(v2), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+                                _ptr(v2), _ptr(ws), _ws_bytes(ws), _stream(stream)),
            "hsa_context_kv")
 
 
@@ -362,12 +369,12 @@ def layer_step(w: "LayerWeights", kcache, vcache, xA, idx, pos, ws, x_src=None, 
         sparsity.check(N, kcache.device)
         _check(lib().hsa_layer_step_sparse(C.byref(w.c), _ptr(kcache), _ptr(vcache), N, _ptr(xA), _ptr(x_src),
                                            _ptr(idx), M, _ptr(pos), _ptr(ctx_k), _ptr(ctx_v), L,
-                                           C.byref(sparsity.c), _ptr(ws), ws.numel() * ws.element_size(),
-                                           _stream(stream)), "hsa_layer_step_sparse")
+                                           C.byref(sparsity.c), _ptr(ws), _ws_bytes(ws), _stream(stream)),
+               "hsa_layer_step_sparse")
         return
     _check(lib().hsa_layer_step(C.byref(w.c), _ptr(kcache), _ptr(vcache), N, _ptr(xA), _ptr(x_src), _ptr(idx), M,
-                                _ptr(pos), _ptr(ctx_k), _ptr(ctx_v), L, _ptr(ws),
-                                ws.numel() * ws.element_size(), _stream(stream)), "hsa_layer_step")
+                                _ptr(pos), _ptr(ctx_k), _ptr(ctx_v), L, _ptr(ws), _ws_bytes(ws), _stream(stream)),
+           "hsa_layer_step")
 
 
 def patch_workspace_size(M: int, D: int, Cc: int, dtype: int) -> int:
@@ -378,15 +385,15 @@ def patch_embed(x, idx, w_in, b_in, X, ws, stream=None):
     N, Cc = x.shape
     D = w_in.shape[0]
     _check(lib().hsa_patch_embed(_ptr(x), _ptr(idx), idx.shape[0], N, Cc, D, _dtype_code(w_in), _ptr(w_in),
-                                 _ptr(b_in), _ptr(X), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+                                 _ptr(b_in), _ptr(X), _ptr(ws), _ws_bytes(ws), _stream(stream)),
            "hsa_patch_embed")
 
 
 def velocity_head(X, head_mod, w_out, b_out, vA, ws, stream=None):
     M, D = X.shape
     _check(lib().hsa_velocity_head(_ptr(X), M, D, w_out.shape[0], _dtype_code(w_out), _ptr(head_mod), _ptr(w_out),
-                                   _ptr(b_out), _ptr(vA), _ptr(ws), ws.numel() * ws.element_size(),
-                                   _stream(stream)), "hsa_velocity_head")
+                                   _ptr(b_out), _ptr(vA), _ptr(ws), _ws_bytes(ws), _stream(stream)),
+           "hsa_velocity_head")
 
 
 def _device_copy(a, device, dtype):
@@ -501,7 +508,7 @@ def block_scores(q, k, H: int, block: int, scores, ws=None, stream=None):
     elif ws.get_device() != dev:
         raise ValueError("ws must be on the operands' device")
     rc = (_lib or load()).hsa_block_scores(q.data_ptr(), M, k.data_ptr(), L, H, code, block, scores.data_ptr(),
-                                           ws.data_ptr(), ws.nbytes, st)
+                                           ws.data_ptr(), _ws_bytes(ws), st)
     if rc:
         raise HsaError(rc, "hsa_block_scores")
 
@@ -548,8 +555,8 @@ def sparse_attention(q, k, v, H: int, block: int, lists, counts, o, stream=None,
     st = _current(dev, stream)
     rc = (_lib or load()).hsa_sparse_attention(q.data_ptr(), M, k.data_ptr(), v.data_ptr(), L, H, code, block,
                                                lists.data_ptr(), keep, counts.data_ptr(), o.data_ptr(),
-                                               None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes,
-                                               st)
+                                               None if ws is None else ws.data_ptr(),
+                                               0 if ws is None else _ws_bytes(ws), st)
     if rc:
         raise HsaError(rc, "hsa_sparse_attention")
 
@@ -642,8 +649,7 @@ def iteration_host(w: "LayerWeights", kcache, vcache, idx, pos, xA, vhat, dsigma
     a = IterationArgsC(C.pointer(w.c), _ptr(kcache), _ptr(vcache), N, _ptr(idx), M, _ptr(pos), _ptr(ctx_k),
                        _ptr(ctx_v), 0 if ctx_k is None else ctx_k.shape[0], _ptr(xA), _ptr(vhat), dsigma,
                        _ptr(score), len(sizes), sizes.ctypes.data, _ptr(group), _ptr(order), _ptr(ws),
-                       ws.numel() * ws.element_size(), _ptr(sel_ws),
-                       0 if sel_ws is None else sel_ws.numel() * sel_ws.element_size())
+                       _ws_bytes(ws), _ptr(sel_ws), 0 if sel_ws is None else _ws_bytes(sel_ws))
     _check(lib().hsa_iteration_host(C.byref(a), h_x_in.data_ptr(), h_x_out.data_ptr(), C.byref(slot.c),
                                     _stream(stream), _stream(stream_h2d), _stream(stream_d2h)),
            "hsa_iteration_host")
