@@ -407,7 +407,8 @@ int hsa_layer_step_sparse(const hsa_layer_weights* w, void* d_kcache, void* d_vc
  * apart (three parts of one [n_mod][6][D] table, say).  Norms: eps 1e-6, LAYER subtracts the mean.
  * NULL gains are 1, NULL offsets 0, a NULL gate 1.  With pre = HSA_NORM_NONE there is no out (d_out, d_mul
  * and d_add NULL).  A row whose token or modulation index is out of range is left as it was and flags
- * HSA_EINDEX.  D % 8 == 0, D <= 12288.  d_X_out may be d_X. */
+ * HSA_EINDEX.  D % 8 == 0, D <= 12288.  d_X_out may be d_X.  Where a wait on the device ran out
+ * (HSA_ETIMEOUT), every row of the outputs is either finished or as it was. */
 enum { HSA_NORM_NONE = 0, HSA_NORM_RMS = 1, HSA_NORM_LAYER = 2 };
 typedef struct hsa_residual_norm_args {
   const float* d_X;             /* M x D float32 residual stream                              */

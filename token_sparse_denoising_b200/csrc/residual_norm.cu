@@ -61,6 +61,27 @@ __device__ __forceinline__ void group_sync(int g) {
   else asm volatile("bar.sync %0, %1;" ::"r"(g), "r"(32 * W) : "memory");
 }
 
+// The same, and whether `x` holds in all of their threads
+template <int W>
+__device__ __forceinline__ bool group_all(int g, bool x) {
+  if constexpr (W == 1) {
+    x = __all_sync(0xffffffffu, x);
+    __syncwarp();
+    return x;
+  } else {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(g), "r"(32 * W)
+        : "memory");
+    return r != 0;
+  }
+}
+
 // Sum over the W warps of a row; the two halves of `part` alternate, so one barrier a sum is enough
 template <int W>
 __device__ __forceinline__ float row_sum(float v, float* part, int& turn, int g) {
@@ -203,9 +224,12 @@ __global__ void __launch_bounds__(32 * kRnWarps, 1) k_residual_norm(const ResNor
       const int col = 4 * (l + c * 32 * W);
       if (col < D) z[c] = fma4(scale, ld4(xs + col), z[c]);
     }
-    // the row is in registers: its slot takes the row `slots` further on
-    group_sync<W>(g);
-    if (l == 0 && r + (int64_t)slots * step < M) load_row(r + (int64_t)slots * step, s);
+    // The row is in registers: its slot takes the row `slots` further on.  Where a thread's wait gave up, none of
+    // the group stores this row or a later one, and no copy is sent to a slot whose last one may not have landed.
+    // (Joined to the barrier: 0.6 % of the whole; a flag in shared memory or leaving the loop 1 to 4 %.)
+    filled = group_all<W>(g, filled);
+    good = good && filled;
+    if (l == 0 && filled && r + (int64_t)slots * step < M) load_row(r + (int64_t)slots * step, s);
     if (++s == slots) {
       s = 0;
       phase ^= 1;
