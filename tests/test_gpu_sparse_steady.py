@@ -30,3 +30,19 @@ def test_residual_norm_rows_are_whole_or_untouched_after_a_stall(cuda_lib, M, D)
     assert bool(((out == want_out).all(1) == done).all()) and bool(((out == 9.0).all(1) == kept).all())
     cuda_lib.residual_norm(X, y, out=out, post="rms", pre="layer")
     assert torch.equal(X, want) and torch.equal(out, want_out) and cuda_lib.device_status() == 0
+
+
+@pytest.mark.parametrize("M,L,H,dtype", [(20000, 9000, 4, torch.bfloat16), (3000, 9000, 5, torch.float32)])
+def test_block_scores_return_after_a_stall_in_the_middle(cuda_lib, M, L, H, dtype):
+    """Several items a CTA and several tiles a range, with the abort flag raised: the call returns, writes its
+    scores and nothing beside them, and the next one is right."""
+    q, k = (dev(S.normal(211 + i, (n, 128 * H)), dtype) for i, n in enumerate((M, L)))
+    shape = (H, -(-M // 128), -(-L // 64))
+    want, guarded = torch.empty(shape, device="cuda"), torch.full((H + 2, *shape[1:]), 9.0, device="cuda")
+    cuda_lib.block_scores(q, k, H, 64, want)
+    cuda_lib.selftest_wait_timeout()
+    cuda_lib.block_scores(q, k, H, 64, guarded[1:-1])
+    assert cuda_lib.device_status() == cuda_lib.HSA_ETIMEOUT
+    assert bool((guarded[0] == 9.0).all()) and bool((guarded[-1] == 9.0).all())
+    cuda_lib.block_scores(q, k, H, 64, guarded[1:-1])
+    assert torch.equal(guarded[1:-1], want) and cuda_lib.device_status() == 0

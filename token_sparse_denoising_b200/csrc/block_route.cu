@@ -80,10 +80,9 @@ __global__ void __launch_bounds__(kMeanThreads, 1)
     const int boxes = (n + 63) >> 6;
     if (warp == 8) {
       for (int b = 0; b < boxes; ++b) {
-        const bool ok = __shfl_sync(0xffffffffu, mbar_wait(&sh->empty[s], phase ^ 1u), 0);
-        good = good && ok;
-        __syncwarp();
-        if (ok && lane == 0) {
+        good = mbar_wait_warp(&sh->empty[s], phase ^ 1u);
+        if (!good) break;
+        if (lane == 0) {
           mbar_expect_tx(&sh->full[s], kMeanBox);
           tma_load_2d(ring + s * kMeanBox, key ? &tmK : &tmQ, &sh->full[s], x, r0 + 64 * b);
         }
@@ -96,8 +95,8 @@ __global__ void __launch_bounds__(kMeanThreads, 1)
     } else if (warp < 8) {
       float sum[V] = {};
       for (int b = 0; b < boxes; ++b) {
-        good = mbar_wait(&sh->full[s], phase) && good;
-        __syncwarp();
+        good = mbar_wait_warp(&sh->full[s], phase);
+        if (!good) break;
         const uint8_t* box = ring + s * kMeanBox + warp * 512 + lane * 16;
         uint4 raw[8];
 #pragma unroll
@@ -121,16 +120,16 @@ __global__ void __launch_bounds__(kMeanThreads, 1)
           phase ^= 1u;
         }
       }
-      good = mbar_wait(&sh->part_empty[ps], pphase ^ 1u) && good;
-      __syncwarp();
+      if (good) good = mbar_wait_warp(&sh->part_empty[ps], pphase ^ 1u);
+      if (!good) break;
 #pragma unroll
       for (int e = 0; e < V; e += 4)
         st4(&sh->part[ps][warp][lane * V + e], make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]));
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->part_full[ps]);
     } else {
-      good = mbar_wait(&sh->part_full[ps], pphase) && good;
-      __syncwarp();
+      good = mbar_wait_warp(&sh->part_full[ps], pphase);
+      if (!good) break;
       const int c = ((warp - 9) * 32 + lane) * 4;
       if (c < 32 * V) {
         float4 t = ld4(&sh->part[ps][0][c]);
@@ -159,6 +158,7 @@ __global__ void __launch_bounds__(kMeanThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->part_empty[ps]);
     }
+    if (!good) break;                                     // the loads' warp
     if (++ps == kMeanParts) {
       ps = 0;
       pphase ^= 1u;
@@ -248,10 +248,9 @@ __global__ void __launch_bounds__(192, 1)
     __syncwarp();
     for (int i = 0; i < nj; ++i) {
       const int b = i & 1;
-      const bool ok = __shfl_sync(0xffffffffu, mbar_wait(&b_empty[b], ((i >> 1) & 1) ^ 1), 0);
-      good = good && ok;
-      __syncwarp();
-      if (ok && leader) {
+      good = mbar_wait_warp(&b_empty[b], ((i >> 1) & 1) ^ 1);
+      if (!good) break;
+      if (leader) {
         mbar_expect_tx(&b_full[b], kProdB);
         for (int p = 0; p < 3; ++p)
           for (int c = 0; c < 2; ++c)
@@ -264,13 +263,11 @@ __global__ void __launch_bounds__(192, 1)
     const bool leader = elect_one();
     constexpr uint32_t idesc = idesc_bf16_f32(128, 64, false);
     const uint64_t ad = sdesc_sw128(smem_u32(smem), 16, 1024), bd = sdesc_sw128(smem_u32(sB), 16, 1024);
-    bool ok = __shfl_sync(0xffffffffu, mbar_wait(&a_full, 0), 0);
-    for (int i = 0; ok && i < nj; ++i) {
+    good = mbar_wait_warp(&a_full, 0);
+    for (int i = 0; good && i < nj; ++i) {
       const int b = i & 1;
-      ok = __shfl_sync(0xffffffffu, mbar_wait(&b_full[b], (i >> 1) & 1), 0);
-      if (ok) ok = __shfl_sync(0xffffffffu, mbar_wait(&d_empty[b], ((i >> 1) & 1) ^ 1), 0);
-      __syncwarp();
-      if (!ok) break;
+      good = mbar_wait_warp(&b_full[b], (i >> 1) & 1) && mbar_wait_warp(&d_empty[b], ((i >> 1) & 1) ^ 1);
+      if (!good) break;
       tc_fence_after();
       if (leader) {
         // smallest pairs first: (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
@@ -289,7 +286,6 @@ __global__ void __launch_bounds__(192, 1)
       }
       __syncwarp();
     }
-    good = ok;
   } else {
     // thread = row of the tile; rows staged 65 floats apart, free of bank conflicts in both directions
     const int quarter = warp & 3;
@@ -298,8 +294,8 @@ __global__ void __launch_bounds__(192, 1)
     const int rows = min(32, n_tiles - t0 - quarter * 32);
     for (int i = 0; i < nj; ++i) {
       const int b = i & 1, b0 = (j0 + i) * 64;
-      good = mbar_wait(&d_full[b], (i >> 1) & 1) && good;
-      __syncwarp();
+      good = mbar_wait_warp(&d_full[b], (i >> 1) & 1);
+      if (!good) break;
       tc_fence_after();
       uint32_t v[64];
       tmem_ld32(tm + ((uint32_t)(quarter * 32) << 16) + b * 64, *reinterpret_cast<uint32_t(*)[32]>(v));

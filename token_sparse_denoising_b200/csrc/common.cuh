@@ -92,6 +92,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// The wait of a whole warp, which goes on together: true where no lane gave up.  A role that gave up arrives on
+// nothing and issues nothing any more: what it would release may still be written or read.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
+  __syncwarp();
+  return ok;
+}
+
 // For a thread whose wait gave up, before it leaves its role: time for the copies and MMAs still in
 // flight to land, so that the CTA does not give up shared memory or TMEM that they write (they take
 // microseconds; 0.1 ms is far more).
