@@ -145,13 +145,6 @@ __device__ __forceinline__ void quad_transpose(uint4 (&c)[4], int lane) {
   }
 }
 
-// The whole warp waits and goes on together
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  const bool r = __shfl_sync(0xffffffffu, mbar_wait(bar, parity), 0);
-  __syncwarp();
-  return r;
-}
-
 __global__ void __launch_bounds__(kSpThreads, 1)
     k_attn_sparse(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, int M, int L, int H, __nv_bfloat16* __restrict__ O,
@@ -229,7 +222,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
           nt = (int)((long long)(split + 1) * nt_all / n_split) - j0;
           if (nt > 0 && ok) {
             // slot free: the unit kSpUnits before it is finished everywhere
-            if (staged >= kSpUnits) ok = warp_wait(&sh->unit_empty[at.s], at.phase ^ 1u);
+            if (staged >= kSpUnits) ok = mbar_wait_warp(&sh->unit_empty[at.s], at.phase ^ 1u);
             const int per = halves ? 2 : 1, first = j0 * per, n = min(nt * per, n_list - first);
             const int* src = sl.list + (size_t)u * sl.keep + first;
             uint16_t* dst = lists + at.s * stride;
@@ -260,7 +253,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
             }
           }
         } else if (staged >= kSpUnits && ok) {
-          ok = warp_wait(&sh->unit_empty[at.s], at.phase ^ 1u);
+          ok = mbar_wait_warp(&sh->unit_empty[at.s], at.phase ^ 1u);
         }
         if (ok && (nt > 0 || cta < 0)) {
           if (lane == 0) sh->unit[at.s] = SparseUnit{u, nt, slot};
@@ -269,13 +262,13 @@ __global__ void __launch_bounds__(kSpThreads, 1)
           at.advance();
           ++staged;
           if (nt >= kSpAheadTiles) {
-            ok = warp_wait(&sh->near_end, end_phase);
+            ok = mbar_wait_warp(&sh->near_end, end_phase);
             end_phase ^= 1u;
           }
         }
         if (cta < 0 || !ok) break;
         if (lane == 0) clc_request(&sh->clc_answer, &sh->clc);
-        ok = warp_wait(&sh->clc, clc_phase);
+        ok = mbar_wait_warp(&sh->clc, clc_phase);
         if (!ok) break;
         clc_phase ^= 1u;
         cta = clc_answer_cta(&sh->clc_answer);
@@ -312,7 +305,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
         if (k_t == k_nt) {
           if (!k_first) kc.advance();
           k_first = false;
-          ok = warp_wait(&sh->unit_full[kc.s], kc.phase);
+          ok = mbar_wait_warp(&sh->unit_full[kc.s], kc.phase);
           const SparseUnit unit = sh->unit[kc.s];
           if (!ok || unit.nt == 0) {
             k_end = true;
@@ -323,7 +316,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
           k_x0 = unit.u / grid.QT * 128;
           k_m0 = unit.u % grid.QT * kAttnBM;
         }
-        ok = warp_wait(&sh->k_empty[k_slot], k_phase);
+        ok = mbar_wait_warp(&sh->k_empty[k_slot], k_phase);
         if (!ok) return false;
         if (leader) load_tile(sK + k_slot * kTileBytes, &tmK, bar, kc.s, k_t, k_x0);
         __syncwarp();
@@ -335,7 +328,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
         if (k_t == 1) {
           // a unit's Q follows its first K: the buffer is free once the last QK^T of the unit before is done,
           // and that wait must not hold up the P barrier that this K completes on
-          if (n_q > 0) ok = warp_wait(&sh->q_empty, (n_q - 1) & 1);
+          if (n_q > 0) ok = mbar_wait_warp(&sh->q_empty, (n_q - 1) & 1);
           if (ok && leader) {
             mbar_expect_tx(&sh->q_full, kTileBytes);
             tma_load_2d(sQ, &tmQ, &sh->q_full, k_x0, k_m0);
@@ -349,14 +342,14 @@ __global__ void __launch_bounds__(kSpThreads, 1)
       if (load_k(&sh->k_full[0])) load_k(&sh->k_full[1]);
       uint32_t g = 0;
       while (ok) {
-        ok = warp_wait(&sh->unit_full[vc.s], vc.phase);
+        ok = mbar_wait_warp(&sh->unit_full[vc.s], vc.phase);
         if (!ok) break;
         const int nt = sh->unit[vc.s].nt, x0 = sh->unit[vc.s].u / grid.QT * 128;
         if (nt == 0) break;
         for (int t = 0; ok && t < nt; ++t, ++g) {
           const uint32_t b = g & 1u;
           if (t == nt - kSpAheadTiles && lane == 0) mbar_arrive(&sh->near_end);
-          ok = warp_wait(&sh->v_empty[b], ((g >> 1) & 1u) ^ 1u);
+          ok = mbar_wait_warp(&sh->v_empty[b], ((g >> 1) & 1u) ^ 1u);
           if (!ok) break;
           if (leader) load_tile(sV + b * kTileBytes, &tmV, &sh->p_full[b][0], vc.s, t, x0);
           __syncwarp();
@@ -386,19 +379,19 @@ __global__ void __launch_bounds__(kSpThreads, 1)
         if (q_t == q_nt) {
           if (!q_first) qc.advance();
           q_first = false;
-          ok = warp_wait(&sh->unit_full[qc.s], qc.phase);
+          ok = mbar_wait_warp(&sh->unit_full[qc.s], qc.phase);
           q_nt = ok ? sh->unit[qc.s].nt : 0;
           if (q_nt == 0) {
             q_end = true;
             return false;
           }
           q_t = 0;
-          ok = warp_wait(&sh->q_full, n_q & 1);
+          ok = mbar_wait_warp(&sh->q_full, n_q & 1);
           ++n_q;
           if (!ok) return false;
         }
         if (g < 2) {
-          ok = warp_wait(&sh->k_full[g], 0);
+          ok = mbar_wait_warp(&sh->k_full[g], 0);
           if (!ok) return false;
         }
         const uint32_t b = g & 1u;
@@ -422,19 +415,19 @@ __global__ void __launch_bounds__(kSpThreads, 1)
       if (issue_qk(0)) issue_qk(1);
       uint32_t g = 0;
       while (ok) {
-        ok = warp_wait(&sh->unit_full[pc.s], pc.phase);
+        ok = mbar_wait_warp(&sh->unit_full[pc.s], pc.phase);
         if (!ok) break;
         const int nt = sh->unit[pc.s].nt;
         if (nt == 0) break;
         // the first PV of a unit overwrites O: the epilogue of the one before has read it
-        if (n_o > 0) ok = warp_wait(&sh->o_free, (n_o - 1) & 1);
+        if (n_o > 0) ok = mbar_wait_warp(&sh->o_free, (n_o - 1) & 1);
         for (int t = 0; ok && t < nt; ++t, ++g) {
           const uint32_t b = g & 1u;
           const uint64_t vd = v_desc + (uint64_t)((b * kTileBytes) >> 4);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             if (!ok) break;
-            ok = warp_wait(&sh->p_full[b][q], (g >> 1) & 1u);
+            ok = mbar_wait_warp(&sh->p_full[b][q], (g >> 1) & 1u);
             if (!ok) break;
             tc_fence_after();
             if (leader) {
@@ -479,7 +472,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
     uint32_t done_first = 0, done_last = 0;               // parities of its first and last tile
     bool ok = true;
     while (ok) {
-      ok = warp_wait(&sh->unit_full[at.s], at.phase);
+      ok = mbar_wait_warp(&sh->unit_full[at.s], at.phase);
       if (!ok) break;
       const int nt = sh->unit[at.s].nt;                   // 0: the end
       const uint16_t* blk = lists + at.s * stride;
@@ -493,7 +486,8 @@ __global__ void __launch_bounds__(kSpThreads, 1)
           const uint32_t pb = (n_unit & 1u) ^ 1u;
           const float(*xm)[128] = sh->xm[pb];
           const float(*xl)[128] = sh->xl[pb];
-          ok = mbar_wait(&sh->merge[quarter], pb) && ok;
+          ok = mbar_wait_warp(&sh->merge[quarter], pb);
+          if (!ok) break;
           const float mF = xm[done_first][row], mG = xm[done_first ^ 1u][row];
           const float mm = fmaxf(mF, mG);
           const float ms = mm == -INFINITY ? 0.f : mm;    // no key at all: weights 0
@@ -504,8 +498,8 @@ __global__ void __launch_bounds__(kSpThreads, 1)
           const int m0 = (done_u % grid.QT) * kAttnBM;
           const bool part = done_slot >= 0 && m0 + row < M;
           if (part && par == 0) grid.part_ml[(size_t)done_slot * kAttnBM + row] = make_float2(mm, den);
-          ok = mbar_wait(&sh->o_done, pb) && ok;
-          __syncwarp();
+          ok = mbar_wait_warp(&sh->o_done, pb);
+          if (!ok) break;
           tc_fence_after();
           // this warp writes output columns [64 par, 64 par + 64) of its 32 rows, 32 at a time
           uint4 ch[2][4];                                 // the row's 64 columns in bf16, chunks of 8
@@ -563,9 +557,9 @@ __global__ void __launch_bounds__(kSpThreads, 1)
           v1 = b1 == kNoBlock ? 0 : L - (int)b1 * sl.block;
           if (!halves) v1 -= 64;
         }
-        ok = mbar_wait(&sh->s_full[par], s_phase) && ok;
+        ok = mbar_wait_warp(&sh->s_full[par], s_phase);
+        if (!ok) break;
         s_phase ^= 1u;
-        __syncwarp();
         tc_fence_after();
         uint32_t sr[128];
 #pragma unroll
@@ -640,7 +634,7 @@ __global__ void __launch_bounds__(kSpThreads, 1)
         }
         t += 2;
       } while (t < nt || done_u >= 0);
-      if (nt == 0) break;
+      if (!ok || nt == 0) break;
       done_u = sh->unit[at.s].u;
       done_slot = sh->unit[at.s].slot;
       done_two = nt >= 2;
@@ -654,7 +648,6 @@ __global__ void __launch_bounds__(kSpThreads, 1)
       first ^= (uint32_t)nt & 1u;
       ++n_unit;
       at.advance();
-      ok = __all_sync(0xffffffffu, ok);
     }
     if (!ok) stall_drain();
   }
