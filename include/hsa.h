@@ -367,7 +367,8 @@ int hsa_block_select(const float* d_scores, int rows, int n_blocks, int keep, co
  * tile.  d_q: M x 128H, d_k, d_v: L x 128H, d_o: M x 128H in dtype; d_list [H][T][keep], d_count [H][T]
  * as hsa_block_select writes them.  Any order of a list is accepted; an index listed twice counts its
  * keys twice; entries behind the count are not read as blocks.  A count of 0 gives rows of 0.
- * B <= 65535.  A listed index outside [0, B) is skipped and a count outside [0, keep] clamped, and both flag HSA_EINDEX.
+ * B <= 65535, 128 H < 2^31, M < 2^31 - 127 and ceil(M / 128) H < 2^30.  A listed index outside [0, B) is skipped
+ * and a count outside [0, keep] clamped, and both flag HSA_EINDEX.
  * With a workspace of hsa_sparse_attention_workspace_size(...) bytes the lists of the last, incomplete
  * wave of work units are split into ranges that a second kernel joins, as in hsa_attention_ws (a few
  * rows against a long list need it); a smaller or NULL workspace runs every list whole.  The size is
@@ -382,7 +383,7 @@ int hsa_sparse_attention(const void* d_q, int M, const void* d_k, const void* d_
  * per tile and head, and the active rows attend to those blocks only:
  *   hsa_block_scores(q, Kc) -> hsa_block_select(keep, d_forced) -> hsa_sparse_attention(q, Kc, Vc).
  * The rest of the step, the arguments and the cross-attention are hsa_layer_step's.  With keep >= the
- * number of blocks every block is listed.  N / block_k <= 16384 blocks.  Workspace:
+ * number of blocks every block is listed.  ceil(N / block_k) <= 16384, H <= 4096.  Workspace:
  * hsa_layer_step_sparse_workspace_size(M, N, D, F, dtype, sp) bytes (0: sp or a size is not allowed), not
  * monotonic in M: a caller that steps on different M takes the largest of their sizes. */
 typedef struct hsa_block_sparsity {

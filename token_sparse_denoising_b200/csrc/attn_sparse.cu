@@ -32,6 +32,8 @@
 //
 // Rounding: logits, running max and sum, and O are float32; p is rounded to bf16 for the second
 // product (its sum is taken before the rounding; at most 2^-8 of each term), and O once at the end.
+#include <climits>
+
 #include "tcgen05.cuh"
 
 namespace hsa {
@@ -915,6 +917,12 @@ __global__ void __launch_bounds__(256) k_attn_sparse_f32_combine(const float* __
 
 // ------------------------------------------------------------------ host
 namespace {
+// Sizes whose work units, rows and columns the kernels can count in an int (the float32 kernel has up to two
+// units per query tile and head)
+bool sparse_sizes_ok(int M, int H) {
+  return M <= INT_MAX - 127 && H <= INT_MAX / 128 && 2LL * ((M + 127) / 128) * H <= INT_MAX;
+}
+
 int sparse_tiles(int keep, int block) { return block == 64 ? (keep + 1) / 2 : keep; }
 
 // Ranges of the lists of an incomplete last wave's units.  Few units (a handful of query rows) against long
@@ -1022,7 +1030,9 @@ int sparse_f32(const float* Q, int M, const float* K, const float* V, int L, int
 using namespace hsa;
 
 extern "C" size_t hsa_sparse_attention_workspace_size(int M, int L, int H, int dtype, int block_k, int keep) {
-  if (M <= 0 || L <= 0 || H <= 0 || keep < 1 || keep > HSA_SPARSE_MAX_KEEP || (block_k != 64 && block_k != 128)) return 0;
+  if (M <= 0 || L <= 0 || H <= 0 || keep < 1 || keep > HSA_SPARSE_MAX_KEEP || (block_k != 64 && block_k != 128) ||
+      !sparse_sizes_ok(M, H))
+    return 0;
   if (dtype == HSA_F32) {
     const int BQ = sparse_f32_rows(M, H, keep), S = sparse_f32_splits(M, H, keep, BQ, ~size_t(0));
     if (S <= 1) return 0;
@@ -1043,11 +1053,12 @@ extern "C" int hsa_sparse_attention(const void* d_q, int M, const void* d_k, con
     return set_error(HSA_EINVAL, "sparse_attention: need 1 <= keep <= 4096");
   if ((L - 1) / block_k >= kSpMaxBlocks)
     return set_error(HSA_EINVAL, "sparse_attention: more than 65535 blocks");
+  if (!sparse_sizes_ok(M, H)) return set_error(HSA_EINVAL, "sparse_attention: M or H too large");
   if (M == 0) return HSA_OK;
   if (!d_q || !d_k || !d_v || !d_o || !d_list || !d_count || !aligned16(d_q) || !aligned16(d_k) || !aligned16(d_v) ||
       !aligned16(d_o) || (d_ws && !aligned16(d_ws)))
     return set_error(HSA_EINVAL, "sparse_attention: null or misaligned pointer");
-  const SparseList sl{d_list, d_count, keep, block_k, (L + block_k - 1) / block_k};
+  const SparseList sl{d_list, d_count, keep, block_k, (L - 1) / block_k + 1};
   cudaStream_t st = as_stream(stream);
   if (dtype == HSA_BF16) return sparse_bf16(d_q, M, d_k, d_v, L, H, sl, d_o, d_ws, ws_bytes, st);
   return sparse_f32(static_cast<const float*>(d_q), M, static_cast<const float*>(d_k), static_cast<const float*>(d_v), L,

@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 32 * W, W == 1 ? (V > 16 ? 3 : 
 template <int W, int V>
 static void launch_select(const float* s, int rows, int n_blocks, int keep, const uint8_t* f, int* list, int* count,
                           cudaStream_t st) {
-  launch(k_block_select<W, V>, W == 1 ? (unsigned)(rows + 7) / 8 : (unsigned)rows, W == 1 ? 256 : 32 * W, 0, st, s, rows,
+  launch(k_block_select<W, V>, W == 1 ? ((unsigned)rows + 7) / 8 : (unsigned)rows, W == 1 ? 256 : 32 * W, 0, st, s, rows,
          n_blocks, keep, f, list, count);
 }
 
@@ -580,7 +580,7 @@ static void launch_select(const float* s, int rows, int n_blocks, int keep, cons
 
 using namespace hsa;
 
-static inline int blocks_of(int n, int size) { return (n + size - 1) / size; }
+static inline int blocks_of(int n, int size) { return n / size + (n % size != 0); }   // n + size may overflow
 
 extern "C" size_t hsa_block_scores_workspace_size(int M, int L, int H, int block_k) {
   if (M <= 0 || L <= 0 || H <= 0 || (block_k != 64 && block_k != 128)) return 0;
