@@ -1,4 +1,6 @@
 """Sizes at the ends of their types: refused, or counted right, before anything reaches a GPU."""
+import ctypes as C
+
 import pytest
 
 from token_sparse_denoising_b200 import build, hsa
@@ -26,3 +28,14 @@ def test_sparse_attention_refuses_what_it_cannot_count(lib, M, H, dtype):
     assert lib.hsa_sparse_attention_workspace_size(M, 1000, H, dtype, 64, 4) == 0
     assert lib.hsa_sparse_attention(FAKE, M, FAKE, FAKE, 1000, H, dtype, 64, FAKE, 4, FAKE, FAKE, None, 0,
                                     None) == hsa.HSA_EINVAL
+
+
+def test_layer_step_sparse_refuses_heads_that_its_scores_would(lib):
+    """Before the cache rows are written: the scores take at most 4096 heads."""
+    sp, H = hsa.BlockSparsityC(64, 4, None), 4097
+    w = hsa.LayerWeightsC(128 * H, H, 512, hsa.HSA_BF16)
+    for name, _ in hsa.LayerWeightsC._fields_[4:15]:
+        setattr(w, name, FAKE)
+    assert lib.hsa_layer_step_sparse_workspace_size(10, 300, 128 * H, 512, hsa.HSA_BF16, C.byref(sp)) == 0
+    assert lib.hsa_layer_step_sparse(C.byref(w), FAKE, FAKE, 300, FAKE, FAKE, FAKE, 10, FAKE, None, None, 0, C.byref(sp),
+                                     FAKE, 1 << 62, None) == hsa.HSA_EINVAL

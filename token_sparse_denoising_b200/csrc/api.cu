@@ -229,9 +229,9 @@ struct SparseWs {
   int32_t *list, *count;
   size_t scores_bytes, attn_bytes, total;
 };
-bool sparsity_ok(const hsa_block_sparsity* sp, int N) {
+bool sparsity_ok(const hsa_block_sparsity* sp, int N, int H) {
   return sp && (sp->block_k == 64 || sp->block_k == 128) && sp->keep >= 1 && sp->keep <= HSA_SPARSE_MAX_KEEP && N > 0 &&
-         (N - 1) / sp->block_k < 16384;
+         (N - 1) / sp->block_k < 16384 && H <= 4096;       // what the scores and the selection take
 }
 SparseWs carve_sparse_ws(void* base, int M, int N, int H, int dtype, const hsa_block_sparsity& sp) {
   const size_t T = ((size_t)M + HSA_QUERY_TILE - 1) / HSA_QUERY_TILE, B = ((size_t)N + sp.block_k - 1) / sp.block_k;
@@ -252,7 +252,7 @@ SparseWs carve_sparse_ws(void* base, int M, int N, int H, int dtype, const hsa_b
 
 extern "C" size_t hsa_layer_step_sparse_workspace_size(int M, int N, int D, int F, int dtype,
                                                        const hsa_block_sparsity* sp) {
-  if (M <= 0 || N < M || D <= 0 || D % 128 || F <= 0 || (dtype != HSA_BF16 && dtype != HSA_F32) || !sparsity_ok(sp, N))
+  if (M <= 0 || N < M || D <= 0 || D % 128 || F <= 0 || (dtype != HSA_BF16 && dtype != HSA_F32) || !sparsity_ok(sp, N, D / 128))
     return 0;
   return hsa_layer_step_workspace_size(M, D, F, dtype) + carve_sparse_ws(nullptr, M, N, D / 128, dtype, *sp).total;
 }
@@ -288,7 +288,7 @@ static int layer_step(const hsa_layer_weights* w, void* d_kcache, void* d_vcache
 
   SparseWs sws = {};
   if (sp) {
-    if (!sparsity_ok(sp, N)) return set_error(HSA_EINVAL, "layer_step: block sparsity out of range");
+    if (!sparsity_ok(sp, N, H)) return set_error(HSA_EINVAL, "layer_step: block sparsity out of range");
     sws = carve_sparse_ws(d_ws, M, N, H, dt, *sp);
     if (ws_bytes < hsa_layer_step_workspace_size(M, D, F, dt) + sws.total)
       return set_error(HSA_EWORKSPACE, "layer_step: workspace smaller than hsa_layer_step_sparse_workspace_size");
