@@ -33,7 +33,8 @@
  *     A wait that ran out also raises a per-device abort flag so that no other
  *     kernel can hang: until hsa_device_status() has been called (which reads
  *     and clears both), every later pipelined kernel on that device (attention,
- *     GEMM) returns early and leaves its outputs incomplete.  A caller that can
+ *     GEMM, block scores, residual norm) returns early and leaves its outputs
+ *     incomplete.  A caller that can
  *     meet a stall should therefore read the status after every step, not only
  *     at the end of a run, to know which step first went wrong.
  *   - Matrices in [out][in] layout (row o holds the weights of output o),
@@ -344,8 +345,9 @@ int hsa_linear(const void* d_x, int M, int Kin, const void* d_w, int Nout, const
  *
  * Scores: the mean logit of a query tile against a block,
  *   d_scores[h][t][b] = (mean of the tile's q rows) . (mean of the block's k rows) / sqrt(128),
- * float32 accuracy (a mean that is not finite gives NaN).  d_q: M x 128H, d_k: L x 128H in dtype;
- * d_scores: [H][T][B] float32.  T + B <= 65535, H <= 4096.  Workspace: hsa_block_scores_workspace_size(M, L, H, block_k) bytes (the means). */
+ * float32 accuracy (a sum of rows or a mean beyond the finite range gives NaN).  d_q: M x 128H, d_k: L x 128H in
+ * dtype; d_scores: [H][T][B] float32.  T + B <= 65535, H <= 4096.  Workspace:
+ * hsa_block_scores_workspace_size(M, L, H, block_k) bytes (the means). */
 enum { HSA_QUERY_TILE = 128, HSA_SPARSE_MAX_KEEP = 4096 };
 size_t hsa_block_scores_workspace_size(int M, int L, int H, int block_k);
 int hsa_block_scores(const void* d_q, int M, const void* d_k, int L, int H, int dtype, int block_k,
@@ -404,7 +406,7 @@ int hsa_layer_step_sparse(const hsa_layer_weights* w, void* d_kcache, void* d_vc
  *   X_out = res_scale X + gate[s] * z
  *   out = pre(X_out) * (1 + mul[s]) + add[s]  (modulate != 0), or pre(X_out) * mul[s] + add[s]
  * with s the row's modulation row: d_mod_row[d_idx[r]] of a table with N entries (d_idx NULL:
- * d_mod_row[r]; d_mod_row NULL: 0).  gate, mul and add point at n_mod rows of D floats, mod_stride floats
+ * d_mod_row[r]; d_mod_row NULL: 0, and d_idx is not read).  gate, mul and add point at n_mod rows of D floats, mod_stride floats
  * apart (three parts of one [n_mod][6][D] table, say).  Norms: eps 1e-6, LAYER subtracts the mean.
  * NULL gains are 1, NULL offsets 0, a NULL gate 1.  With pre = HSA_NORM_NONE there is no out (d_out, d_mul
  * and d_add NULL).  A row whose token or modulation index is out of range is left as it was and flags

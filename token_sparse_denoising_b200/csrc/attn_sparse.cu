@@ -729,8 +729,8 @@ __device__ __forceinline__ void stage_rows(const SparseList& s, size_t unit, int
 // (2 x 4 and 2 x 8 tiles with P row by row, as in k_attn_f32, read three times as much: 22.7 against 16.1 us
 // for 512 rows x 8 of 16 blocks of 64, 2 heads).  Tiles come by 16-byte asynchronous copies: K of the next
 // tile travels while this one's softmax and P V run, V while the next Q K^T does.  BQ = 128 gives an SM eight
-// warps to hide the reads' latency with (2000 x 16 of 63 blocks of 64, 8 heads: 264 us, with 64 rows 308);
-// BQ = 64 makes twice the CTAs, for calls that would leave SMs idle.
+// warps to hide the reads' latency with (2000 x 16 of 63 blocks of 64, 8 heads: 264 us, with 64 rows 307);
+// BQ = 64 makes twice the CTAs, for calls that would leave SMs idle (the rule: sparse_f32_rows).
 constexpr int kSp32BK = 64, kSp32Ld = 132;
 constexpr int sparse_f32_smem(int bq) { return ((bq + 2 * kSp32BK) * kSp32Ld + kSp32BK * (bq + 4)) * 4; }
 static_assert(sparse_f32_smem(128) + 4 * HSA_SPARSE_MAX_KEEP <= 227 * 1024, "the longest list must fit shared memory");
@@ -938,7 +938,11 @@ TailSplit sparse_plan(int M, int H, int keep, int block) {
   return plan_tail(U, tiles, sms);
 }
 
-// The fp32 kernel's query rows per CTA: 128 where that, with the lists split, still fills the SMs
+// The fp32 kernel's query rows per CTA: 128 where the units, cut into at most 32 ranges of a block or more, could
+// make a CTA for every SM.  Ranges are SMs / units rounded down, so 75 to 147 units are not split, and nothing is
+// without a workspace.  Measured with 128 against 64 rows (16 of 63 blocks of 64): 80 or 125 units 263 us against
+// 307, 32 units 72 / 82; 8 units of 20 blocks 41 / 36, of 8 blocks, where the rule says 64, 23 / 16.  Without a
+// workspace 64 rows are faster below 75 units (32 units: 263 / 154), which the rule does not look at.
 int sparse_f32_rows(int M, int H, int keep) {
   const long long units = (long long)((M + 127) / 128) * H;
   return units * (keep < 32 ? keep : 32) >= num_sms() ? 128 : 64;

@@ -642,8 +642,10 @@ extern "C" int hsa_block_select(const float* d_scores, int rows, int n_blocks, i
   if (!d_scores || !d_list || !d_count) return set_error(HSA_EINVAL, "block_select: null pointer");
   cudaStream_t st = as_stream(stream);
   ScopedTiming timing(HSA_KCLASS_OTHER, st);
-  // the fewest warps that hold a row with at most 40 keys a lane (64 keys a lane leave an SM too few warps: 24
-  // million scores in rows of 1500 122 us, with two warps of 24 79), then the next size of the register array
+  // Warps a row and keys a lane: one warp up to 1280 blocks, two up to 2560, four up to 4096, with at most 40 keys
+  // a lane (64 leave an SM too few warps: 24 million scores in rows of 1500 122 us, with two warps of 24 79) and
+  // the next size of the register array; beyond that eight warps, of 32 keys up to 8192 blocks and of 64 above.
+  // At 80 registers a thread the arrays of 40 spill 96 to 148 bytes a thread, the smaller ones at most 64.
   const int v = blocks_of(n_blocks, 32);
   if (v <= 2) launch_select<1, 2>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);
   else if (v <= 4) launch_select<1, 4>(d_scores, rows, n_blocks, keep, d_forced, d_list, d_count, st);

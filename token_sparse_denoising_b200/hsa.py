@@ -492,7 +492,8 @@ def block_scores_workspace_size(M: int, L: int, H: int, block: int) -> int:
 
 def block_scores(q, k, H: int, block: int, scores, ws=None, stream=None):
     """scores[h, t, b] = mean logit of query tile t (128 rows of q) against block b (`block` rows of k),
-    float32 (hsa_block_scores); `ws`: uint8, at least block_scores_workspace_size bytes."""
+    float32 (hsa_block_scores); `ws`: uint8, at least block_scores_workspace_size bytes (None: taken for
+    this call on its stream)."""
     torch = _torch or _use_torch()
     M, L, D, dt, dev = q.shape[0], k.shape[0], H * 128, q.dtype, q.get_device()
     code = _code_of(q)
@@ -572,7 +573,7 @@ def residual_norm(X, y, X_out=None, out=None, b=None, post="none", post_g=None, 
     """X_out = res_scale X + gate * post(y + b); out = pre(X_out) (1 + mul) + add, or pre(X_out) mul + add
     when not `modulate` (hsa_residual_norm).  post, pre: "none", "rms" or "layer"; X_out defaults to X.
     gate, mul, add: [D], or (n_mod, D) views of one modulation table (equal row strides) whose row is
-    mod_row[token], token = idx[r] (idx None: r)."""
+    mod_row[token], token = idx[r] (idx None: r; without mod_row idx is not used)."""
     torch = _torch or _use_torch()
     shape, f32t, dev = X.shape, torch.float32, X.get_device()
     M, D = shape
