@@ -17,9 +17,10 @@
 // and y travel while this row is reduced and written; the copies bypass L1, which keeps the
 // modulation vectors that neighbouring rows share.
 // Measured, 32760 x 1536 (bf16 in and out) / 8190 x 5120 (float32 in, bf16 out), one set of buffers again and
-// again: 103 / 97 us (before the barrier ahead of a refill also told of waits that gave up, 0.5 %); 16 warps of 48 values a thread 111 / 102, 8 warps 127 / 119; a warp per row with plain
-// loads and no ring 150 / 122.  With sets that take turns, so that nothing is left in L2: 108 / 108 us, 5.6 /
-// 5.5 TB/s of the 6.56 a copy reaches; cache hints on the loads or stores and larger rings change that by 2 % at most.
+// again: 103 / 97 us (before the barrier ahead of a refill also told of waits that gave up, 0.5 %); 16 warps of 48
+// values a thread 111 / 102, 8 warps 127 / 119; a warp per row with plain loads and no ring 150 / 122.  With sets
+// that take turns, so that nothing is left in L2: 108 / 108 us, 5.6 / 5.5 TB/s of the 6.56 a copy reaches; cache
+// hints on the loads or stores and larger rings change that by 2 % at most.
 #include "common.cuh"
 
 namespace hsa {
@@ -280,9 +281,9 @@ static int launch_resnorm(const ResNormArgs& a, const void* y, void* out, cudaSt
 }
 
 // W: the fewest warps whose threads hold at most 24 values; C: chunks of 4 columns a thread: six, or four (for one
-// warp two or one) where the row fits them (50 million elements in rows of 1664 / 2048 / 8192: 145 / 118 / 129 us with six, 124 / 106 /
-// 115 with four), and five for eight warps alone (4097 to 5120 columns; the other widths between two thirds and
-// five sixths of six chunks take six)
+// warp two or one) where the row fits them (50 million elements in rows of 1664 / 2048 / 8192: 145 / 118 / 129 us
+// with six, 124 / 106 / 115 with four), and five for eight warps alone (4097 to 5120 columns; the other widths
+// between two thirds and five sixths of six chunks take six)
 template <typename TY, typename TO>
 static int dispatch_resnorm(const ResNormArgs& a, const void* y, void* out, cudaStream_t st) {
   const int D = a.D;
